@@ -2,9 +2,11 @@
 
 y = dequant(Wq) x + alpha * B diag(gamma(A x)) A x with gamma(u) =
 sigmoid(g * u + b) (SPEAR summary, section 2.1 A), computed by hand-written
-HIP kernels behind the C ABI declared in include/spear_ec.h.  This package
-holds the kernels (csrc/), their build script (build.py) and a ctypes binding
-(binding.py) with the same names as the C entry points.  PyTorch is used only
+HIP kernels behind the C ABI declared in include/spear_ec.h, and the 4-bit
+paged key/value cache of include/spear_ec_kv.h: appending, attention and
+reading back.  This package holds the kernels (csrc/), their build script
+(build.py) and a ctypes binding (binding.py, kv.py) with the same names as the
+C entry points.  PyTorch is used only
 to hold device memory and to supply the current stream.
 """
 from .binding import (  # noqa: F401
@@ -19,6 +21,11 @@ from .binding import (  # noqa: F401
     spear_ec_quantize_rtn,
     spear_ec_status_string, spear_ec_version, spear_ec_workspace_bytes,
     spear_ec_workspace_status,
+)
+from .kv import (  # noqa: F401
+    KV_EXPORTED, SPEAR_EC_WS_BAD_PAGE, alloc_kv_cache, alloc_kv_workspace, kv_cache_shapes,
+    make_kv_batch, make_kv_desc, spear_ec_kv_append, spear_ec_kv_attention, spear_ec_kv_batch,
+    spear_ec_kv_dequant_f32, spear_ec_kv_desc, spear_ec_kv_rope, spear_ec_kv_workspace_bytes,
 )
 
 

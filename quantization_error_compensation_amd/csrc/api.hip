@@ -13,7 +13,7 @@ namespace spear {
 
 static thread_local char g_last_error[256] = "";
 
-static int fail(int code, const char* msg) {
+int fail(int code, const char* msg) {
   snprintf(g_last_error, sizeof(g_last_error), "%s", msg);
   return code;
 }
@@ -154,7 +154,9 @@ static Shape make_shape(const spear_ec_desc* d, int T, bool serq = false) {
   return s;
 }
 
-static int hip_status(hipError_t e, const char* what) {
+void clear_error() { g_last_error[0] = 0; }
+
+int hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return SPEAR_EC_OK;
   snprintf(g_last_error, sizeof(g_last_error), "%s: %s", what, hipGetErrorString(e));
   return SPEAR_EC_ERR_HIP;

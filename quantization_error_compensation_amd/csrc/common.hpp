@@ -103,6 +103,35 @@ __device__ __forceinline__ float half_bits_to_f32(uint16_t h) {
   return (float)__builtin_bit_cast(_Float16, h);
 }
 
+// double -> binary16 bits, round to nearest even on the 53-bit significand,
+// finite overflow saturating at 65504 (0x7BFF).
+__device__ __forceinline__ uint16_t f64_to_f16_rne_sat(double v) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(v);
+  const uint16_t sign = (uint16_t)((bits >> 48) & 0x8000u);
+  const uint64_t a = bits & 0x7FFFFFFFFFFFFFFFull;
+  if (a > 0x7FF0000000000000ull) return 0x7E00u;          // NaN
+  if ((a >> 52) == 0) return sign;                         // zero / double subnormal
+  int e = (int)(a >> 52) - 1023;
+  if (e > 15) return sign | 0x7BFFu;
+  const uint64_t m = (a & 0xFFFFFFFFFFFFFull) | (1ull << 52);
+  const int shift = e >= -14 ? 42 : 28 - e;                 // keep 11 bits / count 2^-24 quanta
+  if (shift > 60) return sign;
+  uint64_t keep = m >> shift;
+  const uint64_t rem = m & ((1ull << shift) - 1);
+  const uint64_t half = 1ull << (shift - 1);
+  if (rem > half || (rem == half && (keep & 1))) ++keep;
+  if (e >= -14) {
+    if (keep == 2048) { keep = 1024; ++e; }
+    if (e > 15) return sign | 0x7BFFu;
+    return sign | (uint16_t)((e + 15) << 10) | (uint16_t)(keep - 1024);
+  }
+  return sign | (uint16_t)keep;  // 1024 quanta is the smallest normal, same bits
+}
+
+__device__ __forceinline__ double f16_bits_to_f64(uint16_t h) {
+  return (double)(float)__builtin_bit_cast(_Float16, h);
+}
+
 // Logistic function in the form whose exp() argument is never positive.
 __device__ __forceinline__ float sigmoidf_safe(float z) {
   if (z >= 0.f) return 1.f / (1.f + expf(-z));

@@ -112,6 +112,12 @@ struct LayerArgs {
   bool out_f32 = false;
 };
 
+// Status of a failed check (its text becomes the thread's last error), of a
+// HIP call, and the reset that every entry point starts with (api.hip).
+int fail(int code, const char* msg);
+int hip_status(hipError_t e, const char* what);
+void clear_error();
+
 hipError_t launch_projection(const Shape& s, const LayerArgs& a, const WsPtrs& w,
                              hipStream_t st);
 hipError_t launch_decode(const Shape& s, const LayerArgs& a, const WsPtrs& w, hipStream_t st);

@@ -1,0 +1,203 @@
+"""Python binding of the 4-bit paged key/value cache (include/spear_ec_kv.h).
+
+As in binding.py every spear_ec_kv_* function has the name of the C entry
+point it calls, marshals its arguments and raises on a non-zero status.  Token
+arrays are [tokens, heads, head_dim] tensors whose rows may be strided (slices
+of one projection's output); the functions refuse tensors of another type,
+shape or layout, since the library sees bare pointers.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from .binding import SPEAR_EC_ZEROS, _check, _ptr, _stream, load_library
+
+SPEAR_EC_WS_BAD_PAGE = 2
+
+KV_EXPORTED = (
+    "spear_ec_kv_append", "spear_ec_kv_workspace_bytes", "spear_ec_kv_attention",
+    "spear_ec_kv_dequant_f32",
+)
+
+
+class spear_ec_kv_desc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class spear_ec_kv_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("q_offsets", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
+class spear_ec_kv_rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("rows", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+_kv_lib = None
+
+
+def _lib():
+    global _kv_lib
+    if _kv_lib is None:
+        lib = load_library()
+        P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        DP, BP = ctypes.POINTER(spear_ec_kv_desc), ctypes.POINTER(spear_ec_kv_batch)
+        lib.spear_ec_kv_append.argtypes = [DP, BP, P, i64, P, i64, P, i64,
+                                           ctypes.POINTER(spear_ec_kv_rope), P, P, P, P, i64, P]
+        lib.spear_ec_kv_append.restype = ctypes.c_int
+        lib.spear_ec_kv_workspace_bytes.argtypes = [DP, i32, i32]
+        lib.spear_ec_kv_workspace_bytes.restype = sz
+        lib.spear_ec_kv_attention.argtypes = [DP, BP, P, i64, P, P, P, ctypes.c_float, i32, P, P, P,
+                                              sz, P]
+        lib.spear_ec_kv_attention.restype = ctypes.c_int
+        lib.spear_ec_kv_dequant_f32.argtypes = [DP, BP, P, P, P, P, P, P]
+        lib.spear_ec_kv_dequant_f32.restype = ctypes.c_int
+        _kv_lib = lib
+    return _kv_lib
+
+
+def make_kv_desc(q_heads: int, kv_heads: int, head_dim: int, page_tokens: int, pages: int,
+                 max_pages: int, zeros: bool) -> spear_ec_kv_desc:
+    return spear_ec_kv_desc(q_heads, kv_heads, head_dim, page_tokens, pages, max_pages,
+                            SPEAR_EC_ZEROS if zeros else 0)
+
+
+def make_kv_batch(q_offsets, seq_lens, page_table, tokens: int) -> spear_ec_kv_batch:
+    """The batch of int32 device tensors q_offsets [n + 1] (or None: one row a
+    sequence), seq_lens [n] and page_table [n, max_pages]; keeps them alive."""
+    import torch
+    n = int(seq_lens.shape[0])
+    shapes = ((q_offsets, (n + 1,)), (seq_lens, (n,)),
+              (page_table, (n, int(page_table.shape[1]))))
+    for t, shape in shapes:
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"a batch array must be contiguous int32 of shape {shape}")
+    b = spear_ec_kv_batch(n, int(tokens), None if q_offsets is None else q_offsets.data_ptr(),
+                          seq_lens.data_ptr(), page_table.data_ptr())
+    b.arrays = (q_offsets, seq_lens, page_table)
+    return b
+
+
+def kv_cache_shapes(desc):
+    """Shapes of the cache arrays for a desc: (codes, scales, zeros or None)."""
+    blocks = desc.page_tokens // 16
+    head = (desc.pages, desc.kv_heads, blocks)
+    return ((*head, 16 * desc.head_dim), (*head, 2, 16),
+            (*head, 16) if desc.flags & SPEAR_EC_ZEROS else None)
+
+
+def alloc_kv_cache(desc, device="cuda"):
+    """Device tensors for a cache: codes (uint8), scales (fp16), zeros (uint8) or None."""
+    import torch
+    c, s, z = kv_cache_shapes(desc)
+    return (torch.empty(c, dtype=torch.uint8, device=device),
+            torch.empty(s, dtype=torch.float16, device=device),
+            torch.empty(z, dtype=torch.uint8, device=device) if z else None)
+
+
+def alloc_kv_workspace(desc, n_seqs, tokens, device="cuda"):
+    """Zero-filled workspace for attention calls of up to n_seqs sequences and
+    `tokens` rows."""
+    import torch
+    n = spear_ec_kv_workspace_bytes(desc, n_seqs, tokens)
+    if n == 0:
+        raise ValueError("invalid desc, sequence or token count")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def spear_ec_kv_workspace_bytes(desc, n_seqs: int, tokens: int) -> int:
+    return int(_lib().spear_ec_kv_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(tokens)))
+
+
+def _rows(t, tokens, heads, dim, dtype, name, strided=True):
+    """Row stride of a token array, checked against what the call will read or write."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[0] < tokens or t.shape[1] != heads or \
+            t.shape[2] != dim:
+        raise ValueError(f"{name} must be {dtype} of shape [>= {tokens}, {heads}, {dim}]")
+    st = t.stride()
+    if (st[2] != 1 and dim > 1) or (st[1] != dim and heads > 1) or \
+            (not strided and st[0] != heads * dim and t.shape[0] > 1):
+        raise ValueError(f"{name}'s rows must be contiguous [{heads}, {dim}]")
+    return st[0] if t.shape[0] > 1 else heads * dim
+
+
+def _cache(desc, codes, scales, zeros):
+    c, s, z = kv_cache_shapes(desc)
+    for t, shape, size in ((codes, c, 1), (scales, s, 2), (zeros, z, 1)):
+        if shape is None:
+            continue
+        if t is None or tuple(t.shape) != shape or t.element_size() != size or \
+                not t.is_contiguous():
+            raise ValueError("codes, scales and zeros must have the shapes of kv_cache_shapes(desc)")
+
+
+def _table(desc, batch):
+    arrays = getattr(batch, "arrays", None)
+    if arrays and arrays[2].shape[1] != desc.max_pages:
+        raise ValueError("page_table's rows must have desc.max_pages entries")
+
+
+def spear_ec_kv_append(desc, batch, q, k, v, cos_sin, codes, scales, zeros, q_out,
+                       interleaved=False, stream=None):
+    """Rotate q (to q_out) and k by cos_sin (fp32 [rows, dim], or None) and
+    store k and v in the cache; q and q_out may be None."""
+    import torch
+    n, D = batch.tokens, desc.head_dim
+    _table(desc, batch)
+    _cache(desc, codes, scales, zeros)
+    ks = _rows(k, n, desc.kv_heads, D, torch.bfloat16, "k")
+    vs = _rows(v, n, desc.kv_heads, D, torch.bfloat16, "v")
+    qs = os = 0
+    if q is not None:
+        qs = _rows(q, n, desc.q_heads, D, torch.bfloat16, "q")
+    if q_out is not None:
+        os = _rows(q_out, n, desc.q_heads, D, torch.bfloat16, "q_out")
+    rope = None
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous fp32 [rows, dim]")
+        rope = ctypes.byref(spear_ec_kv_rope(cos_sin.data_ptr(), cos_sin.shape[0],
+                                             cos_sin.shape[1], int(interleaved)))
+    _check(_lib().spear_ec_kv_append(ctypes.byref(desc), ctypes.byref(batch), _ptr(q), qs, _ptr(k),
+                                     ks, _ptr(v), vs, rope, _ptr(codes), _ptr(scales), _ptr(zeros),
+                                     _ptr(q_out), os, _stream(stream)))
+
+
+def spear_ec_kv_attention(desc, batch, q, codes, scales, zeros, softmax_scale, out, workspace,
+                          lse=None, window=0, stream=None):
+    """Attention of q's rows over their sequences' cached tokens, to out (and
+    lse, fp32 [tokens, q_heads])."""
+    import torch
+    n, H, D = batch.tokens, desc.q_heads, desc.head_dim
+    _table(desc, batch)
+    _cache(desc, codes, scales, zeros)
+    qs = _rows(q, n, H, D, torch.bfloat16, "q")
+    _rows(out, n, H, D, torch.bfloat16, "out", strided=False)
+    if lse is not None and (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < n or
+                            lse.shape[1] != H or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous fp32 of shape [>= {n}, {H}]")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_lib().spear_ec_kv_attention(ctypes.byref(desc), ctypes.byref(batch), _ptr(q), qs,
+                                        _ptr(codes), _ptr(scales), _ptr(zeros),
+                                        float(softmax_scale), int(window), _ptr(out), _ptr(lse),
+                                        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def spear_ec_kv_dequant_f32(desc, batch, codes, scales, zeros, k_out, v_out, stream=None):
+    """The batch's rows of the cache as fp32 values [tokens, kv_heads, head_dim]."""
+    import torch
+    n, G, D = batch.tokens, desc.kv_heads, desc.head_dim
+    _table(desc, batch)
+    _cache(desc, codes, scales, zeros)
+    _rows(k_out, n, G, D, torch.float32, "k_out", strided=False)
+    _rows(v_out, n, G, D, torch.float32, "v_out", strided=False)
+    _check(_lib().spear_ec_kv_dequant_f32(ctypes.byref(desc), ctypes.byref(batch), _ptr(codes),
+                                          _ptr(scales), _ptr(zeros), _ptr(k_out), _ptr(v_out),
+                                          _stream(stream)))
