@@ -53,7 +53,7 @@ extern "C" {
  *   kv_heads    1 .. 256
  *   head_dim    64 or 128
  *   page_tokens a power of two, 16 .. 4096
- *   pages       >= 1
+ *   pages       >= 1; pages * kv_heads * page_tokens/16 at most 2^31 - 1
  *   max_pages   >= 1: entries of a page-table row; max_pages * page_tokens,
  *               the longest sequence, is at most 2^30
  *   flags       0 or SPEAR_EC_ZEROS
@@ -149,9 +149,8 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  *   q    bf16, row t at t * q_stride elements, [q_heads][head_dim] in a row
  *   out  bf16 [tokens][q_heads][head_dim], must not overlap q
  *   lse  fp32 [tokens][q_heads], or NULL
- * Products and sums are held in fp32; q enters the matrix cores exactly (as
- * two 8-bit floats, elements below 2^-22 of the row's largest rounded), each
- * probability times its value's scale as two 8-bit floats (2^-10 relative).
+ * Keys meet q exactly, products and sums are held in fp32, and each
+ * probability times its value's scale is rounded to fp16 (2^-11 relative).
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
  * finite and positive.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.

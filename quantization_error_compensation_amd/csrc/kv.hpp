@@ -17,7 +17,7 @@ struct KvShape {
   int page_shift;  // log2(page_tokens)
   int pages, max_pages;
   bool zeros;
-  int group() const { return q_heads / kv_heads; }
+  __host__ __device__ int group() const { return q_heads / kv_heads; }
 };
 
 struct KvBatch {
@@ -57,14 +57,14 @@ struct KvAttentionArgs {
   float* lse;
 };
 
-// Bytes of workspace an attention call needs (counter words, then partials).
-size_t kv_attention_workspace(const KvShape& s, int n_seqs, int tokens);
-
 hipError_t launch_kv_append(const KvShape& s, const KvBatch& b, const KvAppendArgs& a,
                             hipStream_t st);
 hipError_t launch_kv_dequant(const KvShape& s, const KvBatch& b, const KvCache& c, float* k_out,
                              float* v_out, hipStream_t st);
-hipError_t launch_kv_attention(const KvShape& s, const KvBatch& b, const KvAttentionArgs& a,
-                               void* workspace, hipStream_t st);
+// Bytes of workspace (counter words, then partial results) and launch of the
+// attention kernels.
+size_t kv_decode_workspace(const KvShape& s);
+hipError_t launch_kv_decode(const KvShape& s, const KvBatch& b, const KvAttentionArgs& a,
+                            void* workspace, hipStream_t st);
 
 }  // namespace spear

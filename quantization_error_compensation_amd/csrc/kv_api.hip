@@ -26,6 +26,8 @@ int check_kv_desc(const spear_ec_kv_desc* d) {
     return fail(SPEAR_EC_ERR_UNSUPPORTED, "page_tokens must be a power of two, 16 .. 4096");
   if ((int64_t)d->max_pages * d->page_tokens > (int64_t)1 << 30)
     return fail(SPEAR_EC_ERR_UNSUPPORTED, "max_pages * page_tokens must be at most 2^30");
+  if ((int64_t)d->pages * d->kv_heads * (d->page_tokens / 16) > 0x7FFFFFFF)
+    return fail(SPEAR_EC_ERR_UNSUPPORTED, "a cache has at most 2^31 - 1 blocks of 16 tokens and one head");
   return SPEAR_EC_OK;
 }
 
@@ -91,6 +93,8 @@ KvCache make_kv_cache(const KvShape& s, const uint8_t* codes, const void* scales
                  s.zeros ? const_cast<uint8_t*>(zeros) : nullptr};
 }
 
+size_t attention_workspace(const KvShape& s) { return kv_decode_workspace(s); }
+
 }  // namespace
 }  // namespace spear
 
@@ -148,7 +152,7 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
   if (check_kv_desc(desc) != SPEAR_EC_OK || n_seqs < 0 || tokens < 0 || n_seqs > kKvMaxSeqs ||
       tokens > kKvMaxTokens)
     return 0;
-  return kv_attention_workspace(make_kv_shape(desc), n_seqs, tokens);
+  return attention_workspace(make_kv_shape(desc));
 }
 
 int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch* batch,
@@ -174,7 +178,7 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
     return fail(SPEAR_EC_ERR_MISALIGNED, "a pointer is not 16-byte aligned");
   if (!aligned(lse, 4)) return fail(SPEAR_EC_ERR_MISALIGNED, "lse is not 4-byte aligned");
   const KvShape s = make_kv_shape(desc);
-  if (workspace_bytes < kv_attention_workspace(s, batch->n_seqs, batch->tokens))
+  if (workspace_bytes < attention_workspace(s))
     return fail(SPEAR_EC_ERR_WORKSPACE, "workspace is smaller than spear_ec_kv_workspace_bytes()");
   KvAttentionArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -184,7 +188,7 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
   a.window = window;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  return hip_status(launch_kv_attention(s, make_kv_batch(batch), a, workspace, stream),
+  return hip_status(launch_kv_decode(s, make_kv_batch(batch), a, workspace, stream),
                     "cache attention kernel launch");
 }
 

@@ -8,16 +8,14 @@ Tolerances of an attention output are counted from the header's arithmetic,
 with u = 2^-24 half a step of fp32 and p_j = exp(S_j - m) / l:
   * a score is a sum of D products of q with codes up to 15 in magnitude, less
     z times the sum of q, accumulated in fp32 in any order, then a few
-    products: |dS| <= (D + 16) u * scale * s_j * 30 * sum|q|, plus what q's
-    second 8-bit part drops (elements are held to 2^-22 of the row's largest):
-    2^-22 * max|q| * D * 15 * s_j * scale.  A relative error of p_j is at most
-    twice the largest dS, plus a few u for exp;
-  * p_j s_j is held to 2^-10 of itself and, for small ones, to 2^-21 of the
-    largest of its row;
+    products: |dS| <= (D + 16) u * scale * s_j * 30 * sum|q|.  A relative error
+    of p_j is at most twice the largest dS, plus exp's and its argument's
+    rounding, under 2^-18;
+  * p_j s_j is rounded to fp16, half a step: 2^-11 of itself, and for small
+    ones 2^-38 of the row's largest p times its largest s;
   * O's sum runs over products with codes up to 15 and zero-points up to 15,
     in fp32: relative to sum p_j s_j 30, (n/16 + 64) u;
-  * the output is rounded once to bf16: half a step, 2^-8 relative (2^-9 of
-    the next power of two).
+  * the output is rounded once to bf16: half a step, at most 2^-8 relative.
 """
 from __future__ import annotations
 
@@ -172,12 +170,10 @@ def attention(cache, q, offsets, lens, table, scale, window=0):
                     p = e / l
                     out[t, h] = (p * vs[sl]) @ vc[sl]
                     lse[t, h] = m + np.log(l)
-                    aq = np.abs(q[t, h])
-                    dS = (scale * ks[sl].max()
-                          * ((D + 16) * U * 30 * aq.sum() + 2.0 ** -22 * aq.max() * D * 15))
+                    dS = scale * ks[sl].max() * (D + 16) * U * 30 * np.abs(q[t, h]).sum()
                     pv = p * vs[sl]
-                    tol[t, h] = ((2 * dS + 2.0 ** -10 + 2.0 ** -18) * (pv @ np.abs(vc[sl]))
-                                 + 2.0 ** -21 * pv.max() * 15 * m_keys
+                    tol[t, h] = ((2 * dS + 2.0 ** -11 + 2.0 ** -18) * (pv @ np.abs(vc[sl]))
+                                 + 2.0 ** -38 * p.max() * vs[sl].max() * 15 * m_keys
                                  + (m_keys / 16 + 64) * U * 30 * pv.sum())
                     tol[t, h] += half_step_bf16(np.abs(out[t, h]) + tol[t, h])
                     ltol[t, h] = dS + 2.0 ** -20 * (1 + abs(lse[t, h]))

@@ -45,6 +45,7 @@ BAD_DESCS = [
     (dict(head_dim=256), UNSUPPORTED), (dict(page_tokens=8), UNSUPPORTED),
     (dict(page_tokens=48), UNSUPPORTED), (dict(page_tokens=8192), UNSUPPORTED),
     (dict(page_tokens=4096, max_pages=1 << 19), UNSUPPORTED),
+    (dict(pages=1 << 30), UNSUPPORTED),
 ]
 
 
