@@ -7,7 +7,7 @@
  * quantization rules it shares.
  *
  * The cache.  For every (token, kv head) one key and one value vector of
- * head_dim 4-bit codes c, each vector with one fp16 scale s and one zero-point
+ * head_dim 4-bit codes c, each vector with one positive fp16 scale s and one zero-point
  * z (0 .. 15, or 8 throughout without SPEAR_EC_ZEROS); an element stands for
  * (c - z) * s.  Tokens lie in pages of page_tokens; a page holds every kv
  * head's vectors of its tokens.  Three caller-owned device arrays:
@@ -78,7 +78,8 @@ typedef struct spear_ec_kv_desc {
  * means one row per sequence (tokens == n_seqs).  Rows behind
  * q_offsets[n_seqs] belong to no sequence: no call reads or writes them.  A
  * row at a negative position (seq_lens[b] < n) is padding.
- *   n_seqs 0 .. 65536, tokens 0 .. 2^20 (0 of either: nothing is launched)
+ *   n_seqs 0 .. 65536, tokens 0 .. 2^20, tokens * q_heads at most 2^27
+ *   (0 of either count: nothing is launched)
  * Passed by pointer and read during the call only; the three arrays are int32
  * device memory, read by the kernels, so a captured call follows their
  * contents at each replay.
@@ -149,8 +150,8 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  *   q    bf16, row t at t * q_stride elements, [q_heads][head_dim] in a row
  *   out  bf16 [tokens][q_heads][head_dim], must not overlap q
  *   lse  fp32 [tokens][q_heads], or NULL
- * Keys meet q exactly, products and sums are held in fp32, and each
- * probability times its value's scale is rounded to fp16 (2^-11 relative).
+ * Keys meet q exactly and products and sums are held in fp32; a probability
+ * and a value are rounded to fp16 on their way (2^-11 relative each).
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
  * finite and positive.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.

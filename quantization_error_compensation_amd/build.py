@@ -20,7 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libspear_ec.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "static_scratch.hip", "k_quant.hip", "k_proj.hip", "k_decode.hip",
-           "k_prefill.hip", "scheduler.cpp", "kv_api.hip", "k_kv_append.hip", "k_kv_decode.hip"]
+           "k_prefill.hip", "scheduler.cpp", "kv_api.hip", "k_kv_append.hip", "k_kv_decode.hip",
+           "k_kv_prefill.hip"]
 ARCH = os.environ.get("SPEAR_EC_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

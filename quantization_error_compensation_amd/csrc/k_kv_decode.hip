@@ -27,7 +27,7 @@
 // w = 2^(score - M) s stays below 2^14 and is exact to its 11 bits down to
 // 2^-28 of that.  Every sum is fp32.
 #include "internal.hpp"
-#include "kv_device.hpp"
+#include "kv_math.hpp"
 #include "spear_ec_kv.h"
 
 namespace spear {
@@ -37,94 +37,9 @@ constexpr int kUnit = 128;       // tokens of a unit
 constexpr int kRows = 16;        // rows of an item
 constexpr int kGroups = 512;     // workgroups: two per compute unit of gfx950
 constexpr int kWaves = 4;
-constexpr int kMaxChunks = kKvMaxSeqs / 64;
 
 template <int D>
 constexpr int slot_floats() { return kRows * D + 2 * kRows; }
-
-// Cache bytes -> bf16 pairs of 16 + c.  0x4180 is 16.0; its mantissa's top
-// four bits count units.  even: bits 0-3 of each byte, odd: bits 4-7.
-__device__ __forceinline__ uint32_t even16(uint32_t w) { return ((w << 3) & 0x78787878u) | 0x80808080u; }
-__device__ __forceinline__ uint32_t odd16(uint32_t w) { return ((w >> 1) & 0x78787878u) | 0x80808080u; }
-// Bytes 0, 1 and 2, 3 of b, each under a byte of `top`.
-__device__ __forceinline__ uint32_t pair01(uint32_t b, uint32_t top) {
-  return __builtin_amdgcn_perm(b, top, 0x01050004u);
-}
-__device__ __forceinline__ uint32_t pair23(uint32_t b, uint32_t top) {
-  return __builtin_amdgcn_perm(b, top, 0x01070006u);
-}
-
-// Value codes: fp16 bytes of 64 + c (0x5400 is 64.0; the four bits under its
-// byte count units).
-__device__ __forceinline__ uint32_t even64(uint32_t w) { return (w << 4) & 0xF0F0F0F0u; }
-__device__ __forceinline__ uint32_t odd64(uint32_t w) { return w & 0xF0F0F0F0u; }
-
-__device__ __forceinline__ f32x4 mfma16x16x32_f16(u32x4 a, u32x4 b, f32x4 c) {
-  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-// Two fp32 -> fp16 pair, nearest even.
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-  f16x2 r;
-  r.x = (_Float16)a;
-  r.y = (_Float16)b;
-  return __builtin_bit_cast(uint32_t, r);
-}
-
-// Larger halves of two pairs of non-negative fp16 values.
-__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b) {
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
-}
-
-// Two fp32 -> bf16 pair, nearest even.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  bf16x2 r;
-  r.x = (__bf16)a;
-  r.y = (__bf16)b;
-  return __builtin_bit_cast(uint32_t, r);
-}
-
-__device__ __forceinline__ uint64_t div_u64(uint64_t a, uint64_t b) {
-  return ((a | b) >> 32) == 0 ? (uint64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// What the split needs of a sequence.
-struct Seq {
-  int first, n;      // its rows of the batch
-  int len;           // tokens with them
-  int tiles;         // 16-row tiles of a kv head
-  int u0, nb;        // first unit and number of units of its items
-};
-
-__device__ __forceinline__ Seq load_seq(const KvShape& s, const KvBatch& b, int window, int i) {
-  Seq q;
-  int first = i, end = i + 1;
-  if (b.q_offsets) {
-    first = min(max(b.q_offsets[i], 0), b.tokens);
-    end = min(max(b.q_offsets[i + 1], first), b.tokens);
-  }
-  q.first = first;
-  q.n = end - first;
-  q.len = max(b.seq_lens[i], 0);
-  q.tiles = (q.n * s.group() + kRows - 1) / kRows;
-  const int last = min(q.len, s.max_pages << s.page_shift) - 1;
-  const int lo = window ? max(0, min(q.len - q.n - window + 1, last)) : 0;
-  q.u0 = lo / kUnit;
-  q.nb = last < 0 ? 1 : last / kUnit - q.u0 + 1;  // an empty sequence's rows are still written
-  return q;
-}
-
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
 
 // Codes, scales and zero-points of one unit in a lane's registers.
 template <int D, bool ZEROS>
@@ -138,14 +53,17 @@ struct Unit {
 template <int D, bool ZEROS>
 __device__ __forceinline__ void load_keys(Unit<D, ZEROS>& u, const KvCache& c, const int (&blk)[2],
                                           int n, int kb) {
+  #pragma unroll
   for (int t = 0; t < 8; ++t) {
     const uint8_t* p = c.codes + (int64_t)blk[t >> 2] * (16 * D) +
                        ((4 * (t & 3) + (n & 3)) * (D / 2) + kb * (D / 8));
     if constexpr (D == 128) {
       const u32x4 w = load16(p);
+      #pragma unroll
       for (int i = 0; i < 4; ++i) u.k[t][i] = w[i];
     } else {
       const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+      #pragma unroll
       for (int i = 0; i < 2; ++i) u.k[t][i] = w[i];
     }
   }
@@ -154,13 +72,18 @@ __device__ __forceinline__ void load_keys(Unit<D, ZEROS>& u, const KvCache& c, c
 template <int D, bool ZEROS>
 __device__ __forceinline__ void load_values(Unit<D, ZEROS>& u, const KvCache& c,
                                             const int (&blk)[2], int n) {
+  #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint8_t* sp = reinterpret_cast<const uint8_t*>(c.scales) + (int64_t)blk[h] * 64;
+    #pragma unroll
     for (int i = 0; i < 2; ++i) u.ks[h][i] = load16(sp + 16 * i);
+    #pragma unroll
     for (int i = 0; i < 2; ++i) u.vs[h][i] = load16(sp + 32 + 16 * i);
     if constexpr (ZEROS) u.z[h] = load16(c.zeros + (int64_t)blk[h] * 16);
   }
+  #pragma unroll
   for (int t = 0; t < D / 32; ++t)
+    #pragma unroll
     for (int h = 0; h < 2; ++h)
       u.v[t][h] = load16(c.codes + (int64_t)blk[h] * (16 * D) + 8 * D + (16 * t + n) * 16);
 }
@@ -183,21 +106,20 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
   const int n = lane & 15, kb = lane >> 4;
   const int capacity = s.max_pages << s.page_shift;
 
-  // ---- the split: S units a workgroup
-  const int chunks = (b.n_seqs + 63) / 64;
+  // ---- the split: equal runs of units
+  const auto seq_at = [&](int i) { return load_seq<kRows, kUnit>(s, b, a.window, i); };
   int64_t units = 0, items = 0;
   int longest = 0;
-  for (int c = 0; c < chunks; ++c) {
-    if (64 * c + lane < b.n_seqs) {
-      const Seq q = load_seq(s, b, a.window, 64 * c + lane);
-      const int64_t it = (int64_t)q.tiles * s.kv_heads;
-      items += it;
-      units += it * q.nb;
-      if (it) longest = max(longest, q.nb);
-    }
+  for (int i = lane; i < b.n_seqs; i += 64) {
+    const Seq q = seq_at(i);
+    const int64_t it = (int64_t)q.tiles * s.kv_heads;
+    items += it;
+    units += it * q.nb;
+    if (it) longest = max(longest, q.nb);
   }
   units = wave_sum(units);
   items = wave_sum(items);
+  #pragma unroll
   for (int o = 32; o > 0; o >>= 1) longest = max(longest, __shfl_xor(longest, o, 64));
   int64_t run = max((units + kGroups - 1) / kGroups, (int64_t)kWaves);
   // A workgroup per item where that takes at most two more steps of its four
@@ -208,58 +130,18 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
   int64_t x0 = (int64_t)blockIdx.x * run;
   const int64_t x1 = min(x0 + run, total);
   if (x0 >= x1) return;
-  if (chunks > 1) {
-    for (int c = wave; c < chunks; c += kWaves) {
-      int64_t w = 0;
-      if (64 * c + lane < b.n_seqs) {
-        const Seq q = load_seq(s, b, a.window, 64 * c + lane);
-        w = (int64_t)q.tiles * s.kv_heads * (whole ? 1 : q.nb);
-      }
-      w = wave_sum(w);
-      if (lane == 0) before[c + 1] = w;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      before[0] = 0;
-      for (int c = 0; c < chunks; ++c) before[c + 1] += before[c];
-    }
-    __syncthreads();
-  }
+  const auto weight = [&](int i) {
+    const Seq q = seq_at(i);
+    return (int64_t)q.tiles * s.kv_heads * (whole ? 1 : q.nb);
+  };
+  if (b.n_seqs > 64) sum_chunks<kWaves>(before, b.n_seqs, weight);
 
   while (x0 < x1) {
     // ---- the item that holds work x0
-    int chunk = 0;
-    int64_t base = 0;
-    if (chunks > 1) {
-      int lo = 0, hi = chunks;  // before[lo] <= x0 < before[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (before[mid] <= x0) lo = mid; else hi = mid;
-      }
-      chunk = lo;
-      base = before[lo];
-    }
-    Seq q{0, 0, 0, 0, 0, 1};
-    int64_t w = 0;
-    if (64 * chunk + lane < b.n_seqs) {
-      q = load_seq(s, b, a.window, 64 * chunk + lane);
-      w = (int64_t)q.tiles * s.kv_heads * (whole ? 1 : q.nb);
-    }
-    int64_t upto = w;  // inclusive prefix
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t y = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += y;
-    }
-    const int who = __builtin_amdgcn_readfirstlane(
-        __ffsll((unsigned long long)__ballot(base + upto > x0)) - 1);
-    const int seq = 64 * chunk + who;
-    const int64_t seq_base = base + __shfl(upto - w, who, 64);
-    const int first = __builtin_amdgcn_readlane(q.first, who);
-    const int rows_n = __builtin_amdgcn_readlane(q.n, who);
-    const int len = __builtin_amdgcn_readlane(q.len, who);
-    const int tiles = __builtin_amdgcn_readlane(q.tiles, who);
-    const int u0 = __builtin_amdgcn_readlane(q.u0, who);
-    const int nb = __builtin_amdgcn_readlane(q.nb, who);
+    int64_t seq_base;
+    const int seq = find_seq(before, b.n_seqs, x0, weight, seq_base);
+    const Seq q = seq_at(seq);
+    const int first = q.first, rows_n = q.n, len = q.len, tiles = q.tiles, u0 = q.u0, nb = q.nb;
     const int64_t local = x0 - seq_base;
     const int64_t item = whole ? local : (int64_t)div_u64(local, nb);
     const int ub = whole ? 0 : (int)(local - item * nb);
@@ -279,17 +161,20 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
     const uint16_t* qp = a.q + (int64_t)(first + tok) * a.q_stride + qh * D + kb * (D / 4);
     u32x4 qf[D / 32];
     float qs = 0.f;
+    #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const u32x4 r = live ? load16(qp + 8 * i) : u32x4{0, 0, 0, 0};
+      #pragma unroll
       for (int j = 0; j < 4; ++j) qs += bf16_lo(r[j]) + bf16_hi(r[j]);
       qf[i] = x_permute8(r);
     }
     qs += __shfl_xor(qs, 16, 64);
     qs += __shfl_xor(qs, 32, 64);
-    const float f = a.scale * 1.44269504088896340736f;  // scores in powers of two
+    const float f = a.scale * kLog2e;  // scores in powers of two
     // tokens that some row of the tile sees: a unit inside is unmasked
     int all_lo = live ? lo : 0, all_hi = live ? hi : 0x7FFFFFFF;
     int any_lo = live && hi >= lo ? lo : 0x7FFFFFFF, any_hi = live ? hi : -1;
+    #pragma unroll
     for (int o = 1; o < 16; o <<= 1) {
       all_lo = max(all_lo, __shfl_xor(all_lo, o, 64));
       all_hi = min(all_hi, __shfl_xor(all_hi, o, 64));
@@ -301,6 +186,7 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
     float mx = -INFINITY, m = -INFINITY, l = 0.f;  // l: the lane's own tokens
     int ev = 0;
     f32x4 o[D / 32][2];
+    #pragma unroll
     for (int t = 0; t < D / 32; ++t) o[t][0] = o[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     for (int ui = wave; ui < take; ui += kWaves) {
@@ -326,13 +212,16 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       // scores: x = (sum (16 + c) q - (16 + z) sum q) s
       float x[32];
       const float init = (ZEROS ? -16.f : -24.f) * qs;
+      #pragma unroll
       for (int t = 0; t < 8; ++t) {
         f32x4 acc = {init, init, init, init};
+        #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint32_t e = even16(u.k[t][i]), d = odd16(u.k[t][i]), top = 0x41414141u;
           const u32x4 kf = {pair01(e, top), pair23(e, top), pair01(d, top), pair23(d, top)};
           acc = mfma16x16x32(kf, qf[i], acc);
         }
+        #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float v = acc[i];
           if constexpr (ZEROS)
@@ -341,25 +230,31 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
         }
       }
       if (bads & 0xFF) {  // tokens on a page outside the cache: NaN where they are seen
+        #pragma unroll
         for (int h = 0; h < 2; ++h)
           if ((bads >> (2 * kb + h)) & 1)
+            #pragma unroll
             for (int i = 0; i < 16; ++i) x[16 * h + i] = __uint_as_float(0x7FC00000u);
       }
       const bool masked = j0 < all_lo || j0 + kUnit - 1 > all_hi;
       if (masked) {
+        #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int j = j0 + 32 * kb + i;
           if (j < lo || j > hi) x[i] = -INFINITY;
         }
       }
       float top = x[0];
+      #pragma unroll
       for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
       uint32_t big_s = 0;  // largest value scale (fp16 bits) of the lane's tokens
       if (!masked) {
         uint32_t p = u.vs[0][0][0];
+        #pragma unroll
         for (int i = 1; i < 16; ++i) p = max_pairs(p, u.vs[i >> 3][(i >> 2) & 1][i & 3]);
         big_s = max(p & 0xFFFFu, p >> 16);
       } else {  // an unwritten slot's scale may be anything
+        #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const uint32_t w = u.vs[i >> 4][(i >> 3) & 1][(i >> 1) & 3];
           if (x[i] != -INFINITY) big_s = max(big_s, (i & 1) ? w >> 16 : w & 0xFFFFu);
@@ -373,17 +268,20 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       ev = max(ev, (int)((big_s & 0x7FFFu) >> 10));
       const float mn = mx + (float)(ev - 28);  // scale < 2^(ev - 14)
       if (__any(mn != m)) {
-        const float alpha = mn == m ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
         l *= alpha;
+        #pragma unroll
         for (int t = 0; t < D / 32; ++t)
+          #pragma unroll
           for (int h = 0; h < 2; ++h) o[t][h] *= alpha;
         m = mn;
       }
       const float ref = m == -INFINITY ? 0.f : m;
       u32x4 pf[4];  // probabilities times value scales, 8 tokens a step
+      #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], f, -ref));
-        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i + 1], f, -ref));
+        const float p0 = fast_exp2(__builtin_fmaf(x[i], f, -ref));
+        const float p1 = fast_exp2(__builtin_fmaf(x[i + 1], f, -ref));
         l += p0 + p1;
         float w0 = p0 * scale_of(u.vs, i), w1 = p1 * scale_of(u.vs, i + 1);
         if (masked) {
@@ -393,6 +291,7 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
         pf[i >> 3][(i >> 1) & 3] = pack_f16(w0, w1);
       }
       f32x4 off = {0.f, 0.f, 0.f, 0.f};
+      #pragma unroll
       for (int st = 0; st < 4; ++st) {
         const int h = st >> 1, d0 = 2 * (st & 1);
         u32x4 zf = {0xD480D480u, 0xD480D480u, 0xD480D480u, 0xD480D480u};  // -72
@@ -401,6 +300,7 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
           zf = u32x4{pair01(a0, neg), pair23(a0, neg), pair01(a1, neg), pair23(a1, neg)};
         }
         off = mfma16x16x32_f16(zf, pf[st], off);
+        #pragma unroll
         for (int t = 0; t < D / 32; ++t) {
           const uint32_t w0 = u.v[t][h][d0], w1 = u.v[t][h][d0 + 1], top64 = 0x54545454u;
           const uint32_t e0 = even64(w0), e1 = even64(w1), o0 = odd64(w0), o1 = odd64(w1);
@@ -410,11 +310,14 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
           o[t][1] = mfma16x16x32_f16(odd, pf[st], o[t][1]);
         }
       }
+      #pragma unroll
       for (int t = 0; t < D / 32; ++t)
+        #pragma unroll
         for (int h = 0; h < 2; ++h) o[t][h] += off;
       if ((bads & 0xFF) && lane == 0) {
         // only a token that some row sees makes an output NaN
         bool seen = false;
+        #pragma unroll
         for (int i = 0; i < 8; ++i)
           if ((bads >> i) & 1) seen |= j0 + 16 * i <= any_hi && j0 + 16 * i + 15 >= any_lo;
         if (seen) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
@@ -431,10 +334,12 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
     __syncthreads();
     {
       const float big = fmaxf(fmaxf(msh[0][n], msh[1][n]), fmaxf(msh[2][n], msh[3][n]));
-      const float k = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - big);
+      const float k = m == -INFINITY ? 0.f : fast_exp2(m - big);
+      #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
         // byte columns 16 t + 4 kb + i: eight dimensions in a row
         float* dst = &osh[wave][n][32 * t + 8 * kb];
+        #pragma unroll
         for (int i = 0; i < 4; ++i) {
           dst[2 * i] = o[t][0][i] * k;
           dst[2 * i + 1] = o[t][1][i] * k;
@@ -447,10 +352,12 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
     float acc[kPer];
     float big = -INFINITY, sum = 0.f;
     for (int w2 = 0; w2 < kWaves; ++w2) big = fmaxf(big, msh[w2][r]);
+    #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
     for (int w2 = 0; w2 < kWaves; ++w2) {
       const float mw = msh[w2][r], lw = lsh[w2][r];
-      sum += mw == -INFINITY ? lw : lw * __builtin_amdgcn_exp2f(mw - big);
+      sum += mw == -INFINITY ? lw : lw * fast_exp2(mw - big);
+      #pragma unroll
       for (int i = 0; i < kPer; ++i) acc[i] += osh[w2][r][d0 + i];
     }
 
@@ -466,6 +373,7 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       const uint32_t stride = slot_floats<D>() * 4;
       const uint32_t to = (2 * blockIdx.x + (x0 == (int64_t)blockIdx.x * run ? 0 : 1)) * stride;
       if (mine) {
+        #pragma unroll
         for (int i = 0; i < kPer; i += 4)
           bstore16_dev(rs, to + (r * D + d0 + i) * 4, 0,
                        f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]});
@@ -493,15 +401,18 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
           big = fmaxf(big, bload_dev(rs, from + (kRows * D + r) * 4, 0));
         }
         sum = 0.f;
+        #pragma unroll
         for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
         for (int w2 = wa; w2 <= wb; ++w2) {
           const uint32_t from = (w2 == wa ? first_slot : 2 * w2) * stride;
           const float mw = bload_dev(rs, from + (kRows * D + r) * 4, 0);
           const float lw = bload_dev(rs, from + (kRows * D + kRows + r) * 4, 0);
-          const float k = mw == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mw - big);  // an empty piece is zeros
+          const float k = mw == -INFINITY ? 1.f : fast_exp2(mw - big);  // an empty piece is zeros
           sum += lw * k;
+          #pragma unroll
           for (int i = 0; i < kPer; i += 4) {
             const u32x4 v = bload16_dev(rs, from + (r * D + d0 + i) * 4, 0);
+            #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i + j] += __uint_as_float(v[j]) * k;
           }
         }
@@ -515,11 +426,13 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       float inv = sum == 0.f ? 0.f : 1.f / sum;
       if (past) inv = sum = __uint_as_float(0x7FC00000u);
       uint32_t out[kPer / 2];
+      #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) out[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D + d0);
+      #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) dst[i] = out[i];
       if ((threadIdx.x & 15) == 0) {
-        if (a.lse) a.lse[at] = (big + log2f(sum)) * 0.69314718055994530942f;
+        if (a.lse) a.lse[at] = (big + log2f(sum)) * kLn2;
         if (past) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
       }
     }

@@ -66,5 +66,8 @@ hipError_t launch_kv_dequant(const KvShape& s, const KvBatch& b, const KvCache& 
 size_t kv_decode_workspace(const KvShape& s);
 hipError_t launch_kv_decode(const KvShape& s, const KvBatch& b, const KvAttentionArgs& a,
                             void* workspace, hipStream_t st);
+size_t kv_prefill_workspace(const KvShape& s);
+hipError_t launch_kv_prefill(const KvShape& s, const KvBatch& b, const KvAttentionArgs& a,
+                             void* workspace, hipStream_t st);
 
 }  // namespace spear

@@ -31,12 +31,14 @@ int check_kv_desc(const spear_ec_kv_desc* d) {
   return SPEAR_EC_OK;
 }
 
-int check_kv_batch(const spear_ec_kv_batch* b) {
+int check_kv_batch(const spear_ec_kv_desc* d, const spear_ec_kv_batch* b) {
   if (!b) return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "batch is NULL");
   if (b->n_seqs < 0 || b->tokens < 0)
     return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "batch has a negative count");
   if (b->n_seqs > kKvMaxSeqs || b->tokens > kKvMaxTokens)
     return fail(SPEAR_EC_ERR_UNSUPPORTED, "at most 65536 sequences and 2^20 rows");
+  if ((int64_t)b->tokens * d->q_heads > (int64_t)1 << 27)
+    return fail(SPEAR_EC_ERR_UNSUPPORTED, "tokens * q_heads must be at most 2^27");
   if (b->n_seqs == 0 || b->tokens == 0) return SPEAR_EC_OK;
   if (!b->seq_lens || !b->page_table)
     return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "seq_lens and page_table are required");
@@ -93,7 +95,19 @@ KvCache make_kv_cache(const KvShape& s, const uint8_t* codes, const void* scales
                  s.zeros ? const_cast<uint8_t*>(zeros) : nullptr};
 }
 
-size_t attention_workspace(const KvShape& s) { return kv_decode_workspace(s); }
+// Rows (token, query head of one kv head) a sequence has on average above
+// which a call takes the kernel for many rows.
+constexpr int kDecodeRows = 64;
+
+bool many_rows(const KvShape& s, int n_seqs, int tokens) {
+  return (int64_t)tokens * s.group() > (int64_t)kDecodeRows * n_seqs;
+}
+
+// Covers every call of at most n_seqs sequences and `tokens` rows.
+size_t attention_workspace(const KvShape& s, int tokens) {
+  const size_t d = kv_decode_workspace(s), p = kv_prefill_workspace(s);
+  return many_rows(s, 1, tokens) && p > d ? p : d;
+}
 
 }  // namespace
 }  // namespace spear
@@ -108,7 +122,7 @@ int spear_ec_kv_append(const spear_ec_kv_desc* desc, const spear_ec_kv_batch* ba
                        uint8_t* zeros, void* q_out, int64_t q_out_stride, hipStream_t stream) {
   clear_error();
   int rc = check_kv_desc(desc);
-  if (!rc) rc = check_kv_batch(batch);
+  if (!rc) rc = check_kv_batch(desc, batch);
   if (rc) return rc;
   if (rope) {
     if (rope->rows <= 0 || rope->dim <= 0 || !rope->cos_sin)
@@ -152,7 +166,7 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
   if (check_kv_desc(desc) != SPEAR_EC_OK || n_seqs < 0 || tokens < 0 || n_seqs > kKvMaxSeqs ||
       tokens > kKvMaxTokens)
     return 0;
-  return attention_workspace(make_kv_shape(desc));
+  return attention_workspace(make_kv_shape(desc), tokens);
 }
 
 int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch* batch,
@@ -162,7 +176,7 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
                           size_t workspace_bytes, hipStream_t stream) {
   clear_error();
   int rc = check_kv_desc(desc);
-  if (!rc) rc = check_kv_batch(batch);
+  if (!rc) rc = check_kv_batch(desc, batch);
   if (rc) return rc;
   if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f)
     return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "softmax_scale must be finite and positive");
@@ -178,7 +192,7 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
     return fail(SPEAR_EC_ERR_MISALIGNED, "a pointer is not 16-byte aligned");
   if (!aligned(lse, 4)) return fail(SPEAR_EC_ERR_MISALIGNED, "lse is not 4-byte aligned");
   const KvShape s = make_kv_shape(desc);
-  if (workspace_bytes < attention_workspace(s))
+  if (workspace_bytes < attention_workspace(s, batch->tokens))
     return fail(SPEAR_EC_ERR_WORKSPACE, "workspace is smaller than spear_ec_kv_workspace_bytes()");
   KvAttentionArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -188,7 +202,8 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
   a.window = window;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  return hip_status(launch_kv_decode(s, make_kv_batch(batch), a, workspace, stream),
+  const auto launch = many_rows(s, batch->n_seqs, batch->tokens) ? launch_kv_prefill : launch_kv_decode;
+  return hip_status(launch(s, make_kv_batch(batch), a, workspace, stream),
                     "cache attention kernel launch");
 }
 
@@ -197,7 +212,7 @@ int spear_ec_kv_dequant_f32(const spear_ec_kv_desc* desc, const spear_ec_kv_batc
                             float* k_out, float* v_out, hipStream_t stream) {
   clear_error();
   int rc = check_kv_desc(desc);
-  if (!rc) rc = check_kv_batch(batch);
+  if (!rc) rc = check_kv_batch(desc, batch);
   if (rc) return rc;
   if (batch->n_seqs == 0 || batch->tokens == 0) return SPEAR_EC_OK;
   rc = check_kv_cache(desc, codes, scales, zeros);

@@ -11,8 +11,10 @@ with u = 2^-24 half a step of fp32 and p_j = exp(S_j - m) / l:
     products: |dS| <= (D + 16) u * scale * s_j * 30 * sum|q|.  A relative error
     of p_j is at most twice the largest dS, plus exp's and its argument's
     rounding, under 2^-18;
-  * p_j s_j is rounded to fp16, half a step: 2^-11 of itself, and for small
-    ones 2^-38 of the row's largest p times its largest s;
+  * p_j s_j, or p_j and v_j apart, are rounded to fp16, half a step: 2^-11 of
+    themselves each.  Below fp16's normal range half a step is 2^-25 of what 1
+    stands for: of a value, 2^-25 of the largest scale of its 16 tokens; of a
+    p_j s_j, 2^-25 of the row's largest p times its largest s;
   * O's sum runs over products with codes up to 15 and zero-points up to 15,
     in fp32: relative to sum p_j s_j 30, (n/16 + 64) u;
   * the output is rounded once to bf16: half a step, at most 2^-8 relative.
@@ -172,8 +174,8 @@ def attention(cache, q, offsets, lens, table, scale, window=0):
                     lse[t, h] = m + np.log(l)
                     dS = scale * ks[sl].max() * (D + 16) * U * 30 * np.abs(q[t, h]).sum()
                     pv = p * vs[sl]
-                    tol[t, h] = ((2 * dS + 2.0 ** -11 + 2.0 ** -18) * (pv @ np.abs(vc[sl]))
-                                 + 2.0 ** -38 * p.max() * vs[sl].max() * 15 * m_keys
+                    tol[t, h] = ((2 * dS + 2.0 ** -10 + 2.0 ** -18) * (pv @ np.abs(vc[sl]))
+                                 + 2.0 ** -25 * (p.max() * vs[sl].max() * 15 * m_keys + vs[sl].max())
                                  + (m_keys / 16 + 64) * U * 30 * pv.sum())
                     tol[t, h] += half_step_bf16(np.abs(out[t, h]) + tol[t, h])
                     ltol[t, h] = dS + 2.0 ** -20 * (1 + abs(lse[t, h]))

@@ -93,6 +93,8 @@ def test_descs_and_batches_are_checked(lib, name):
     assert call(lib, name, good, batch(tokens=-1)) == INVALID
     assert call(lib, name, good, batch(n=65537, tokens=65537)) == UNSUPPORTED
     assert call(lib, name, good, batch(tokens=(1 << 20) + 1, off=ptr(22))) == UNSUPPORTED
+    many = q.make_kv_desc(**{**GOOD, "q_heads": 256})
+    assert call(lib, name, many, batch(tokens=(1 << 19) + 1, off=ptr(22))) == UNSUPPORTED
     assert call(lib, name, good, batch(lens=None)) == INVALID
     assert call(lib, name, good, batch(table=None)) == INVALID
     assert call(lib, name, good, batch(tokens=3)) == INVALID          # needs q_offsets
