@@ -4,28 +4,32 @@
 //
 // Work.  The rows (token, query head) of a sequence that read one kv head are
 // taken 16 at a time; an item is one such row tile and one kv head, a unit 128
-// tokens of an item.  Workgroups take equal runs of units (the lengths are
-// device data, so every workgroup adds them up itself), the four waves of a
-// workgroup every fourth unit of a run.  Runs cut items: each workgroup that
-// holds a piece of a cut item leaves (O, m, l) in its slot of the workspace
-// and the last one to arrive joins them in workgroup order, so results do not
-// depend on the order of arrival.
+// tokens of an item.  The lengths are device data, so every workgroup adds them
+// up itself.  Either each item is cut into the same number of pieces, one a
+// workgroup, or, where uneven lengths would make the longest piece more than a
+// step longer than an even share, the workgroups take equal runs of all items'
+// units laid end to end.  The four waves of a workgroup take every fourth unit.
+// Each workgroup that holds a piece of a cut item leaves (O, M, l) in its slot
+// of the workspace, and the last one to arrive joins them in order, so results
+// do not depend on the order of arrival.
 //
 // Matrix cores.  Scores come as S^T = K q^T (16x16x32, bf16): a lane then
 // holds one query row and 32 of the unit's 128 tokens, so the softmax's
 // maximum and sum need two exchanges per unit, and the probabilities are
 // already the operand of O^T = V^T P^T: lane and token order agree because
-// key tile t, row m is token 32 (m / 4) + 4 t + m % 4.  A key's code c becomes
-// the bf16 value 16 + c, a value's the fp16 value 64 + c (its nibble under the
-// top of the mantissa, one byte permute a pair); the offset 16 + z comes out
-// with the row's sum of q for keys, and for values with one matrix step of
-// -(64 + z) against the same probabilities, added once a unit, so that it
-// never grows with the sequence.  Keys and q meet exactly.  A probability
+// key tile t, row m is token 32 (m / 4) + 4 t + m % 4.  Codes become bf16
+// (keys) and fp16 (values) operands by the 8-bit float conversions: a code c
+// alone in its byte is the 8-bit float c 2^-9.  The zero-point comes out with
+// the row's sum of q for keys, and for values with one matrix step of z
+// against the same probabilities, subtracted once a unit, so that it never
+// grows with the sequence.  Keys and q meet exactly.  A probability
 // times its value's scale is rounded to fp16 (2^-11 relative, an eighth of the
 // output's bf16 rounding): the running reference M is the rows' maximum score
 // plus the exponent of the largest value scale so far, less 14, so that
 // w = 2^(score - M) s stays below 2^14 and is exact to its 11 bits down to
 // 2^-28 of that.  Every sum is fp32.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "kv_math.hpp"
 #include "spear_ec_kv.h"
@@ -35,8 +39,9 @@ namespace {
 
 constexpr int kUnit = 128;       // tokens of a unit
 constexpr int kRows = 16;        // rows of an item
-constexpr int kGroups = 512;     // workgroups: two per compute unit of gfx950
-constexpr int kWaves = 4;
+constexpr int kGroups = 256;     // workgroups: one per compute unit of gfx950
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
 
 template <int D>
 constexpr int slot_floats() { return kRows * D + 2 * kRows; }
@@ -88,99 +93,225 @@ __device__ __forceinline__ void load_values(Unit<D, ZEROS>& u, const KvCache& c,
       u.v[t][h] = load16(c.codes + (int64_t)blk[h] * (16 * D) + 8 * D + (16 * t + n) * 16);
 }
 
-// fp16 scale of the lane's token i (0 .. 31) of the unit.
-__device__ __forceinline__ float scale_of(const u32x4 (&s)[2][2], int i) {
+// Product of an fp32 value and the lane's token i's fp16 scale (0 .. 31 of the
+// unit), the half taken from its pair by the instruction.
+__device__ __forceinline__ float times_scale(float v, const u32x4 (&s)[2][2], int i) {
   const uint32_t w = s[i >> 4][(i >> 3) & 1][(i >> 1) & 3];
-  return half_bits_to_f32((uint16_t)((i & 1) ? w >> 16 : w));
+  // with an addend of +0 this is one mixed-precision instruction
+  return __builtin_fmaf(v, half_bits_to_f32((uint16_t)((i & 1) ? w >> 16 : w)), 0.f);
 }
 
-template <int D, bool ZEROS>
-__global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvBatch b,
+// N consecutive floats of a piece, to and from every XCD (device scope).
+template <int N>
+__device__ __forceinline__ void store_piece(rsrc_t rs, uint32_t at, const float (&v)[N]) {
+  if constexpr (N == 4)
+    bstore16_dev(rs, at, 0, f32x4{v[0], v[1], v[2], v[3]});
+  else
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])}, rs, at, 0,
+                                          kDeviceScope);
+}
+template <int N>
+__device__ __forceinline__ void load_piece(rsrc_t rs, uint32_t at, float (&v)[N]) {
+  if constexpr (N == 4) {
+    const u32x4 w = bload16_dev(rs, at, 0);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  } else {
+    const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, kDeviceScope);
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+  }
+}
+
+// a / b of non-negative counts.
+__device__ __forceinline__ int quotient(int a, int b) { return (int)((uint32_t)a / (uint32_t)b); }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) { return (int64_t)div_u64(a, b); }
+
+// Where a workgroup's next piece of work lies.
+struct Piece {
+  int seq, head, tile;
+  int ub, take;           // its units of the item
+  int parts, part;        // pieces the item is cut into, this one's number
+  int counter;            // arrival counter of the item (its first workgroup)
+  int slot0, slot1;       // slots of piece 0 and 1; the others follow by 2
+};
+
+template <int D, bool ZEROS, bool SMALL>
+__global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s, KvBatch b,
                                                                   KvAttentionArgs a, int* counters,
                                                                   float* slots, uint32_t slot_bytes) {
-  __shared__ int64_t before[kMaxChunks + 1];  // work before each 64 sequences
+  __shared__ int64_t before[SMALL ? 1 : kMaxChunks + 1];  // work before each 64 sequences
   __shared__ float osh[kWaves][kRows][D + 4];
-  __shared__ float msh[kWaves][kRows], lsh[kWaves][kRows];
+  __shared__ float msh[kRows][kRows], lsh[kRows][kRows];
   __shared__ int flag;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int n = lane & 15, kb = lane >> 4;
   const int capacity = s.max_pages << s.page_shift;
+  const int group = s.group();
 
-  // ---- the split: equal runs of units
+  // ---- the split
   const auto seq_at = [&](int i) { return load_seq<kRows, kUnit>(s, b, a.window, i); };
-  int64_t units = 0, items = 0;
+  using count_t = typename std::conditional<SMALL, int, int64_t>::type;
+  count_t units = 0, items = 0;
   int longest = 0;
-  for (int i = lane; i < b.n_seqs; i += 64) {
-    const Seq q = seq_at(i);
-    const int64_t it = (int64_t)q.tiles * s.kv_heads;
-    items += it;
-    units += it * q.nb;
-    if (it) longest = max(longest, q.nb);
+  Seq own{0, 0, 0, 0, 0, 1};  // SMALL: the lane's sequence
+  count_t upto_items = 0, upto_units = 0;
+  if constexpr (SMALL) {
+    if (lane < b.n_seqs) own = seq_at(lane);
+    const int it = own.tiles * s.kv_heads;
+    upto_items = wave_prefix(it);
+    upto_units = wave_prefix(it * own.nb);
+    items = __builtin_amdgcn_readlane(upto_items, 63);
+    units = __builtin_amdgcn_readlane(upto_units, 63);
+    longest = wave_max(it ? own.nb : 0);
+  } else {
+    for (int i = lane; i < b.n_seqs; i += 64) {
+      const Seq q = seq_at(i);
+      const int64_t it = (int64_t)q.tiles * s.kv_heads;
+      items += it;
+      units += it * q.nb;
+      if (it) longest = max(longest, q.nb);
+    }
+    units = wave_sum(units);
+    items = wave_sum(items);
+    longest = wave_max(longest);
   }
-  units = wave_sum(units);
-  items = wave_sum(items);
-  #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) longest = max(longest, __shfl_xor(longest, o, 64));
-  int64_t run = max((units + kGroups - 1) / kGroups, (int64_t)kWaves);
-  // A workgroup per item where that takes at most two more steps of its four
-  // waves than the even split: nothing is cut and nothing joined.
-  const bool whole = items <= gridDim.x && longest <= 4 * ((run + 3) / 4 + 2);
-  if (whole) run = 1;  // counted in items
-  const int64_t total = whole ? items : units;
-  int64_t x0 = (int64_t)blockIdx.x * run;
-  const int64_t x1 = min(x0 + run, total);
+  if (items == 0) return;
+  const count_t run = max((count_t)((units + kGroups - 1) / kGroups), (count_t)kWaves);
+  // k pieces an item: as many as there are workgroups for, then as few as
+  // take no more steps of the four waves
+  int k = 0;
+  if (items <= kGroups) {
+    k = kGroups / (int)items;
+    const int even = (int)((run + kWaves - 1) / kWaves);
+    const int steps = ((longest + k - 1) / k + kWaves - 1) / kWaves;
+    if (steps <= even + 1) k = (longest + kWaves * steps - 1) / (kWaves * steps);
+    else
+      k = 0;
+  }
+  count_t x0 = k ? (count_t)(blockIdx.x / k) : (count_t)blockIdx.x * run;
+  const count_t x1 = k ? min(x0 + 1, items) : min(x0 + run, units);
   if (x0 >= x1) return;
   const auto weight = [&](int i) {
     const Seq q = seq_at(i);
-    return (int64_t)q.tiles * s.kv_heads * (whole ? 1 : q.nb);
+    return (int64_t)q.tiles * s.kv_heads * (k ? 1 : q.nb);
   };
-  if (b.n_seqs > 64) sum_chunks<kWaves>(before, b.n_seqs, weight);
+  if constexpr (!SMALL)
+    if (b.n_seqs > 64) sum_chunks<kWaves>(before, b.n_seqs, weight);
 
   while (x0 < x1) {
-    // ---- the item that holds work x0
-    int64_t seq_base;
-    const int seq = find_seq(before, b.n_seqs, x0, weight, seq_base);
-    const Seq q = seq_at(seq);
-    const int first = q.first, rows_n = q.n, len = q.len, tiles = q.tiles, u0 = q.u0, nb = q.nb;
-    const int64_t local = x0 - seq_base;
-    const int64_t item = whole ? local : (int64_t)div_u64(local, nb);
-    const int ub = whole ? 0 : (int)(local - item * nb);
-    const int take = whole ? nb : (int)min((int64_t)(nb - ub), x1 - x0);
-    const int head = (int)div_u64(item, tiles);
-    const int tile = (int)(item - (int64_t)head * tiles);
+    // ---- the piece that starts with work x0
+    Seq q;
+    Piece pc;
+    count_t seq_base;
+    if constexpr (SMALL) {
+      const count_t upto = k ? upto_items : upto_units;
+      const int who = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(upto > x0)) - 1);
+      pc.seq = who;
+      q.first = __builtin_amdgcn_readlane(own.first, who);
+      q.n = __builtin_amdgcn_readlane(own.n, who);
+      q.len = __builtin_amdgcn_readlane(own.len, who);
+      q.tiles = __builtin_amdgcn_readlane(own.tiles, who);
+      q.u0 = __builtin_amdgcn_readlane(own.u0, who);
+      q.nb = __builtin_amdgcn_readlane(own.nb, who);
+      seq_base = __builtin_amdgcn_readlane(upto, who) - q.tiles * s.kv_heads * (k ? 1 : q.nb);
+    } else {
+      int64_t base;
+      pc.seq = find_seq(before, b.n_seqs, x0, weight, base);
+      seq_base = base;
+      q = seq_at(pc.seq);
+    }
+    const int nb = q.nb;
+    const count_t local = x0 - seq_base;
+    count_t item;
+    if (k) {
+      item = local;
+      const int c = (nb + k - 1) / k;
+      pc.part = (int)(blockIdx.x % k);
+      pc.parts = (nb + c - 1) / c;
+      pc.ub = pc.part * c;
+      pc.take = min(c, nb - pc.ub);
+      pc.counter = (int)blockIdx.x - pc.part;
+      pc.slot0 = 2 * pc.counter;
+      pc.slot1 = pc.slot0 + 2;
+      if (pc.take <= 0) return;
+    } else {
+      item = quotient(local, (count_t)nb);
+      pc.ub = (int)(local - item * nb);
+      pc.take = (int)min((count_t)(nb - pc.ub), x1 - x0);
+      const count_t i0 = seq_base + item * nb;  // the item's units
+      const int wa = (int)quotient(i0, run), wb = (int)quotient(i0 + nb - 1, run);
+      pc.part = (int)blockIdx.x - wa;
+      pc.parts = wb - wa + 1;
+      pc.counter = wa;
+      // a workgroup's first piece takes its slot 0, an item it starts later slot 1
+      pc.slot0 = 2 * wa + (i0 == (count_t)wa * run ? 0 : 1);
+      pc.slot1 = 2 * (wa + 1);
+    }
+    pc.head = (int)quotient(item, (count_t)q.tiles);
+    pc.tile = (int)(item - (count_t)pc.head * q.tiles);
+    const int rows_n = q.n * group, start = q.len - q.n;
+    const int rows = min(kRows, rows_n - pc.tile * kRows);  // rows of the tile
 
     // ---- the lane's query row
-    const int group = s.group();
-    const int row = tile * kRows + n;
-    const bool live = row < rows_n * group;
-    const int tok = live ? row / group : 0;
-    const int qh = head * group + (live ? row - tok * group : 0);
-    const int pos = live ? len - rows_n + tok : -1;
+    const bool live = n < rows;
+    const int row = pc.tile * kRows + (live ? n : 0);
+    const int tok = row / group;
+    const int qh = pc.head * group + row - tok * group;
+    const int pos = live ? start + tok : -1;
     const int hi = min(pos, capacity - 1);
     const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-    const uint16_t* qp = a.q + (int64_t)(first + tok) * a.q_stride + qh * D + kb * (D / 4);
+    const uint16_t* qp = a.q + (int64_t)(q.first + tok) * a.q_stride + qh * D + kb * (D / 4);
     u32x4 qf[D / 32];
+    #pragma unroll
+    for (int i = 0; i < D / 32; ++i) qf[i] = live ? load16(qp + 8 * i) : u32x4{0, 0, 0, 0};
+    // tokens that every row, and that some row of the tile sees (its rows are
+    // consecutive tokens; padding rows see none)
+    const int first_pos = start + pc.tile * kRows / group;
+    const int last_pos = start + (pc.tile * kRows + rows - 1) / group;
+    const int all_hi = min(first_pos, capacity - 1);
+    const int all_lo = a.window && last_pos >= a.window ? last_pos - a.window + 1 : 0;
+    const int any_hi = min(last_pos, capacity - 1);
+    const int any_lo = a.window && first_pos >= a.window
+                           ? min(first_pos - a.window + 1, max(any_hi, 0)) : 0;
+
+    // the unit's 8 blocks, one lane each; positions nobody sees stand for the
+    // nearest one that somebody does
+    const int per = 1 << (s.page_shift - 4);
+    const auto block_of = [&](int ui) {
+      if (any_hi < 0) return 0;
+      const int at = min(max((q.u0 + pc.ub + ui) * kUnit + 16 * (lane & 7), any_lo & ~15), any_hi);
+      const int page = b.page_table[(int64_t)pc.seq * s.max_pages + (at >> s.page_shift)];
+      return (unsigned)page < (unsigned)s.pages
+                 ? (page * s.kv_heads + pc.head) * per + ((at >> 4) & (per - 1)) : -1;
+    };
+    const auto spread = [&](int my, int (&kblk)[2], int (&vblk)[2]) {
+      my = max(my, 0);
+      kblk[0] = __shfl(my, 2 * (n >> 2), 64);
+      kblk[1] = __shfl(my, 2 * (n >> 2) + 1, 64);
+      vblk[0] = __shfl(my, 2 * kb, 64);
+      vblk[1] = __shfl(my, 2 * kb + 1, 64);
+    };
+    Unit<D, ZEROS> u;
+    int kblk[2], vblk[2];
+    uint64_t bads = 0;
+    int next = 0;
+    if (wave < pc.take) {
+      const int my = block_of(wave);
+      bads = __ballot(my < 0) & 0xFF;
+      spread(my, kblk, vblk);
+      load_keys(u, a.cache, kblk, n, kb);
+      if (wave + kWaves < pc.take) next = block_of(wave + kWaves);
+    }
     float qs = 0.f;
     #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const u32x4 r = live ? load16(qp + 8 * i) : u32x4{0, 0, 0, 0};
       #pragma unroll
-      for (int j = 0; j < 4; ++j) qs += bf16_lo(r[j]) + bf16_hi(r[j]);
-      qf[i] = x_permute8(r);
+      for (int j = 0; j < 4; ++j) qs += bf16_lo(qf[i][j]) + bf16_hi(qf[i][j]);
+      qf[i] = x_permute8(qf[i]);
     }
-    qs += __shfl_xor(qs, 16, 64);
-    qs += __shfl_xor(qs, 32, 64);
+    qs = join32(join16(qs, sum2), sum2);
     const float f = a.scale * kLog2e;  // scores in powers of two
-    // tokens that some row of the tile sees: a unit inside is unmasked
-    int all_lo = live ? lo : 0, all_hi = live ? hi : 0x7FFFFFFF;
-    int any_lo = live && hi >= lo ? lo : 0x7FFFFFFF, any_hi = live ? hi : -1;
-    #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      all_lo = max(all_lo, __shfl_xor(all_lo, o, 64));
-      all_hi = min(all_hi, __shfl_xor(all_hi, o, 64));
-      any_lo = min(any_lo, __shfl_xor(any_lo, o, 64));
-      any_hi = max(any_hi, __shfl_xor(any_hi, o, 64));
-    }
 
     // mx, ev: the row's largest score and value-scale exponent; m: their reference M
     float mx = -INFINITY, m = -INFINITY, l = 0.f;  // l: the lane's own tokens
@@ -189,36 +320,19 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
     #pragma unroll
     for (int t = 0; t < D / 32; ++t) o[t][0] = o[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int ui = wave; ui < take; ui += kWaves) {
-      const int j0 = (u0 + ub + ui) * kUnit;
-      // the unit's 8 blocks, one lane each; positions nobody sees stand for
-      // the nearest one that somebody does
-      int my = 0;
-      bool bad = false;
-      if (any_hi >= any_lo) {
-        const int at = min(max(j0 + 16 * (lane & 7), any_lo & ~15), any_hi);
-        const int page = b.page_table[(int64_t)seq * s.max_pages + (at >> s.page_shift)];
-        bad = (unsigned)page >= (unsigned)s.pages;
-        const int per = 1 << (s.page_shift - 4);
-        my = bad ? 0 : (page * s.kv_heads + head) * per + ((at >> 4) & (per - 1));
-      }
-      const uint64_t bads = __ballot(bad);
-      const int kblk[2] = {__shfl(my, 2 * (n >> 2), 64), __shfl(my, 2 * (n >> 2) + 1, 64)};
-      const int vblk[2] = {__shfl(my, 2 * kb, 64), __shfl(my, 2 * kb + 1, 64)};
-      Unit<D, ZEROS> u;
-      load_keys(u, a.cache, kblk, n, kb);
+    for (int ui = wave; ui < pc.take; ui += kWaves) {
+      const int j0 = (q.u0 + pc.ub + ui) * kUnit;
+      const bool more = ui + kWaves < pc.take;
       load_values(u, a.cache, vblk, n);
-
-      // scores: x = (sum (16 + c) q - (16 + z) sum q) s
       float x[32];
-      const float init = (ZEROS ? -16.f : -24.f) * qs;
+      const float init = (ZEROS ? 0.f : -8.f) * qs;
       #pragma unroll
       for (int t = 0; t < 8; ++t) {
         f32x4 acc = {init, init, init, init};
         #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint32_t e = even16(u.k[t][i]), d = odd16(u.k[t][i]), top = 0x41414141u;
-          const u32x4 kf = {pair01(e, top), pair23(e, top), pair01(d, top), pair23(d, top)};
+          const uint32_t e = low_codes(u.k[t][i]), d = high_codes(u.k[t][i]);
+          const u32x4 kf = {bf16_01(e), bf16_23(e), bf16_01(d), bf16_23(d)};
           acc = mfma16x16x32(kf, qf[i], acc);
         }
         #pragma unroll
@@ -226,42 +340,47 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
           float v = acc[i];
           if constexpr (ZEROS)
             v -= (float)((u.z[t >> 2][t & 3] >> (8 * i)) & 15u) * qs;
-          x[4 * t + i] = v * scale_of(u.ks, 4 * t + i);
+          x[4 * t + i] = times_scale(v, u.ks, 4 * t + i);
         }
       }
-      if (bads & 0xFF) {  // tokens on a page outside the cache: NaN where they are seen
+      const uint64_t bad = bads;
+      if (more) {  // the next keys arrive during the softmax
+        bads = __ballot(next < 0) & 0xFF;
+        spread(next, kblk, vblk);
+        load_keys(u, a.cache, kblk, n, kb);
+      }
+      if (bad) {  // tokens on a page outside the cache: NaN where they are seen
         #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if ((bads >> (2 * kb + h)) & 1)
+          if ((bad >> (2 * kb + h)) & 1)
             #pragma unroll
             for (int i = 0; i < 16; ++i) x[16 * h + i] = __uint_as_float(0x7FC00000u);
+        bool seen = false;
+        for (int i = 0; i < 8; ++i)
+          if ((bad >> i) & 1) seen |= j0 + 16 * i <= any_hi && j0 + 16 * i + 15 >= any_lo;
+        if (seen && lane == 0) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
       }
       const bool masked = j0 < all_lo || j0 + kUnit - 1 > all_hi;
+      uint32_t big_s = 0;  // largest value scale (fp16 bits) of the lane's tokens
       if (masked) {
         #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int j = j0 + 32 * kb + i;
+          const uint32_t w = u.vs[i >> 4][(i >> 3) & 1][(i >> 1) & 3];
           if (j < lo || j > hi) x[i] = -INFINITY;
+          else big_s = max(big_s, (i & 1) ? w >> 16 : w & 0xFFFFu);  // elsewhere it may be anything
         }
-      }
-      float top = x[0];
-      #pragma unroll
-      for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
-      uint32_t big_s = 0;  // largest value scale (fp16 bits) of the lane's tokens
-      if (!masked) {
+      } else {
         uint32_t p = u.vs[0][0][0];
         #pragma unroll
         for (int i = 1; i < 16; ++i) p = max_pairs(p, u.vs[i >> 3][(i >> 2) & 1][i & 3]);
         big_s = max(p & 0xFFFFu, p >> 16);
-      } else {  // an unwritten slot's scale may be anything
-        #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t w = u.vs[i >> 4][(i >> 3) & 1][(i >> 1) & 3];
-          if (x[i] != -INFINITY) big_s = max(big_s, (i & 1) ? w >> 16 : w & 0xFFFFu);
-        }
       }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      float top = x[0];
+      #pragma unroll
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+      top = join32(join16(top, larger), larger);
+      // half bits order like their values, and are denormal floats: joined as integers
       big_s = max(big_s, (uint32_t)__shfl_xor((int)big_s, 16, 64));
       big_s = max(big_s, (uint32_t)__shfl_xor((int)big_s, 32, 64));
       mx = fmaxf(mx, top * f);
@@ -283,7 +402,7 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
         const float p0 = fast_exp2(__builtin_fmaf(x[i], f, -ref));
         const float p1 = fast_exp2(__builtin_fmaf(x[i + 1], f, -ref));
         l += p0 + p1;
-        float w0 = p0 * scale_of(u.vs, i), w1 = p1 * scale_of(u.vs, i + 1);
+        float w0 = times_scale(p0, u.vs, i), w1 = times_scale(p1, u.vs, i + 1);
         if (masked) {
           w0 = p0 == 0.f ? 0.f : w0;
           w1 = p1 == 0.f ? 0.f : w1;
@@ -294,37 +413,32 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       #pragma unroll
       for (int st = 0; st < 4; ++st) {
         const int h = st >> 1, d0 = 2 * (st & 1);
-        u32x4 zf = {0xD480D480u, 0xD480D480u, 0xD480D480u, 0xD480D480u};  // -72
+        u32x4 zf = {0x48004800u, 0x48004800u, 0x48004800u, 0x48004800u};  // 8
         if constexpr (ZEROS) {
-          const uint32_t a0 = odd64(u.z[h][d0]), a1 = odd64(u.z[h][d0 + 1]), neg = 0xD4D4D4D4u;
-          zf = u32x4{pair01(a0, neg), pair23(a0, neg), pair01(a1, neg), pair23(a1, neg)};
+          const uint32_t a0 = high_codes(u.z[h][d0]);
+          const uint32_t a1 = high_codes(u.z[h][d0 + 1]);
+          zf = u32x4{f16_01(a0), f16_23(a0), f16_01(a1), f16_23(a1)};
         }
         off = mfma16x16x32_f16(zf, pf[st], off);
         #pragma unroll
         for (int t = 0; t < D / 32; ++t) {
-          const uint32_t w0 = u.v[t][h][d0], w1 = u.v[t][h][d0 + 1], top64 = 0x54545454u;
-          const uint32_t e0 = even64(w0), e1 = even64(w1), o0 = odd64(w0), o1 = odd64(w1);
-          const u32x4 evn = {pair01(e0, top64), pair23(e0, top64), pair01(e1, top64), pair23(e1, top64)};
-          const u32x4 odd = {pair01(o0, top64), pair23(o0, top64), pair01(o1, top64), pair23(o1, top64)};
+          const uint32_t w0 = u.v[t][h][d0], w1 = u.v[t][h][d0 + 1];
+          const uint32_t e0 = low_codes(w0), e1 = low_codes(w1), o0 = high_codes(w0), o1 = high_codes(w1);
+          const u32x4 evn = {f16_01(e0), f16_23(e0), f16_01(e1), f16_23(e1)};
+          const u32x4 odd = {f16_01(o0), f16_23(o0), f16_01(o1), f16_23(o1)};
           o[t][0] = mfma16x16x32_f16(evn, pf[st], o[t][0]);
           o[t][1] = mfma16x16x32_f16(odd, pf[st], o[t][1]);
         }
       }
+      if (more) {
+        if (ui + 2 * kWaves < pc.take) next = block_of(ui + 2 * kWaves);
+      }
       #pragma unroll
       for (int t = 0; t < D / 32; ++t)
         #pragma unroll
-        for (int h = 0; h < 2; ++h) o[t][h] += off;
-      if ((bads & 0xFF) && lane == 0) {
-        // only a token that some row sees makes an output NaN
-        bool seen = false;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((bads >> i) & 1) seen |= j0 + 16 * i <= any_hi && j0 + 16 * i + 15 >= any_lo;
-        if (seen) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
-      }
+        for (int h = 0; h < 2; ++h) o[t][h] -= off;
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
+    l = join32(join16(l, sum2), sum2);
 
     // ---- the four waves' results joined
     if (kb == 0) {
@@ -333,51 +447,52 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
     }
     __syncthreads();
     {
-      const float big = fmaxf(fmaxf(msh[0][n], msh[1][n]), fmaxf(msh[2][n], msh[3][n]));
-      const float k = m == -INFINITY ? 0.f : fast_exp2(m - big);
+      float big = msh[0][n];
+      #pragma unroll
+      for (int w = 1; w < kWaves; ++w) big = fmaxf(big, msh[w][n]);
+      const float kf = m == -INFINITY ? 0.f : fast_exp2(m - big);
       #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
         // byte columns 16 t + 4 kb + i: eight dimensions in a row
         float* dst = &osh[wave][n][32 * t + 8 * kb];
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          dst[2 * i] = o[t][0][i] * k;
-          dst[2 * i + 1] = o[t][1][i] * k;
+          dst[2 * i] = o[t][0][i] * kf;
+          dst[2 * i + 1] = o[t][1][i] * kf;
         }
       }
     }
     __syncthreads();
-    constexpr int kPer = D / 16;  // elements a thread finishes
-    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kPer;
+    constexpr int kLanes = kThreads / kRows, kPer = D / kLanes;  // threads a row, elements a thread
+    int r = threadIdx.x / kLanes;
+    const int d0 = (threadIdx.x % kLanes) * kPer;
     float acc[kPer];
     float big = -INFINITY, sum = 0.f;
-    for (int w2 = 0; w2 < kWaves; ++w2) big = fmaxf(big, msh[w2][r]);
+    #pragma unroll
+    for (int w = 0; w < kWaves; ++w) big = fmaxf(big, msh[w][r]);
     #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    for (int w2 = 0; w2 < kWaves; ++w2) {
-      const float mw = msh[w2][r], lw = lsh[w2][r];
+    #pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = msh[w][r], lw = lsh[w][r];
       sum += mw == -INFINITY ? lw : lw * fast_exp2(mw - big);
       #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += osh[w2][r][d0 + i];
+      for (int i = 0; i < kPer; ++i) acc[i] += osh[w][r][d0 + i];
     }
 
     // ---- a piece of a cut item: leave it, and join the pieces if it is the last
-    const int my_row = tile * kRows + r;
-    const bool mine = my_row < rows_n * group;
+    bool mine = r < rows;
     bool last = true;
-    if (take < nb) {
-      const int64_t i0 = seq_base + item * nb;              // the item's units
-      const int wa = (int)div_u64(i0, run);
-      const int wb = (int)div_u64(i0 + nb - 1, run);
+    if (pc.parts > 1) {
       const rsrc_t rs = make_rsrc(slots, slot_bytes);
       const uint32_t stride = slot_floats<D>() * 4;
-      const uint32_t to = (2 * blockIdx.x + (x0 == (int64_t)blockIdx.x * run ? 0 : 1)) * stride;
+      const auto at_slot = [&](int i) {
+        return (uint32_t)(i == 0 ? pc.slot0 : pc.slot1 + 2 * (i - 1)) * stride;
+      };
       if (mine) {
-        #pragma unroll
-        for (int i = 0; i < kPer; i += 4)
-          bstore16_dev(rs, to + (r * D + d0 + i) * 4, 0,
-                       f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]});
-        if ((threadIdx.x & 15) == 0) {
+        const uint32_t to = at_slot(pc.part);
+        store_piece<kPer>(rs, to + (r * D + d0) * 4, acc);
+        if (threadIdx.x % kLanes == 0) {
           bstore_dev(rs, to + (kRows * D + r) * 4, 0, big);
           bstore_dev(rs, to + (kRows * D + kRows + r) * 4, 0, sum);
         }
@@ -385,44 +500,86 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       wait_vmem();
       __syncthreads();
       if (threadIdx.x == 0) {
-        int* ctr = counters + kCtrBand + wa;
+        int* ctr = counters + kCtrBand + pc.counter;
         const int arrived = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        flag = arrived == wb - wa;
-        if (arrived == wb - wa) store_dev(ctr, 0);
+        flag = arrived == pc.parts - 1;
+        if (arrived == pc.parts - 1) store_dev(ctr, 0);
       }
       __syncthreads();
       last = flag != 0;
-      if (last && mine) {
-        // the first piece starts its item inside workgroup wa's run, or with it
-        const uint32_t first_slot = 2 * wa + (i0 == (int64_t)wa * run ? 0 : 1);
+      if (last) {
+        // kLanes threads a row; with few rows the pieces are dealt to `teams` of them
+        int rp = kRows;
+        while (rp > 1 && rows <= rp / 2) rp /= 2;
+        const int teams = kRows / rp, team = r / rp;
+        const int my = r;
+        r &= rp - 1;
+        const int rr = min(r, rows - 1);  // rows past the tile's load another's
         big = -INFINITY;
-        for (int w2 = wa; w2 <= wb; ++w2) {
-          const uint32_t from = (w2 == wa ? first_slot : 2 * w2) * stride;
-          big = fmaxf(big, bload_dev(rs, from + (kRows * D + r) * 4, 0));
-        }
         sum = 0.f;
         #pragma unroll
         for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-        for (int w2 = wa; w2 <= wb; ++w2) {
-          const uint32_t from = (w2 == wa ? first_slot : 2 * w2) * stride;
-          const float mw = bload_dev(rs, from + (kRows * D + r) * 4, 0);
-          const float lw = bload_dev(rs, from + (kRows * D + kRows + r) * 4, 0);
-          const float k = mw == -INFINITY ? 1.f : fast_exp2(mw - big);  // an empty piece is zeros
-          sum += lw * k;
+        constexpr int kBatch = 4;  // pieces in flight
+        for (int p = team; p < pc.parts; p += kBatch * teams) {
+          float ms[kBatch], ls[kBatch];
+          float v[kBatch][kPer];
           #pragma unroll
-          for (int i = 0; i < kPer; i += 4) {
-            const u32x4 v = bload16_dev(rs, from + (r * D + d0 + i) * 4, 0);
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i + j] += __uint_as_float(v[j]) * k;
+          for (int i = 0; i < kBatch; ++i) {
+            const uint32_t from = at_slot(min(p + i * teams, pc.parts - 1));
+            ms[i] = bload_dev(rs, from + (kRows * D + rr) * 4, 0);
+            ls[i] = bload_dev(rs, from + (kRows * D + kRows + rr) * 4, 0);
+            load_piece<kPer>(rs, from + (rr * D + d0) * 4, v[i]);
           }
+          float bn = big;
+          #pragma unroll
+          for (int i = 0; i < kBatch; ++i) bn = fmaxf(bn, ms[i]);
+          if (bn != big) {
+            const float kf = fast_exp2(big - bn);
+            sum *= kf;
+            #pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] *= kf;
+            big = bn;
+          }
+          #pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            // an empty piece is zeros (or NaN); one counted twice counts once
+            float kf = ms[i] == -INFINITY ? 1.f : fast_exp2(ms[i] - big);
+            if (p + i * teams < pc.parts) {
+              sum += ls[i] * kf;
+              #pragma unroll
+              for (int j = 0; j < kPer; ++j) acc[j] += v[i][j] * kf;
+            }
+          }
+        }
+        if (teams > 1) {  // the teams' results, in order
+          float* flat = &osh[0][0][0];
+          #pragma unroll
+          for (int i = 0; i < kPer; ++i) flat[my * D + d0 + i] = acc[i];
+          if (threadIdx.x % kLanes == 0) {
+            msh[team][r] = big;
+            lsh[team][r] = sum;
+          }
+          __syncthreads();
+          big = -INFINITY;
+          sum = 0.f;
+          for (int t = 0; t < teams; ++t) big = fmaxf(big, msh[t][r]);
+          #pragma unroll
+          for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+          for (int t = 0; t < teams; ++t) {
+            const float kf = msh[t][r] == -INFINITY ? 1.f : fast_exp2(msh[t][r] - big);
+            sum += lsh[t][r] * kf;
+            #pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] += flat[(t * rp + r) * D + d0 + i] * kf;
+          }
+          mine = team == 0 && r < rows;
         }
       }
     }
     if (last && mine) {
-      const int t = my_row / group;
-      const int h = head * group + my_row - t * group;
-      const int64_t at = (int64_t)(first + t) * s.q_heads + h;
-      const bool past = len - rows_n + t >= capacity;  // longer than its page-table row
+      const int out_row = pc.tile * kRows + r;
+      const int t = out_row / group;
+      const int64_t at = (int64_t)(q.first + t) * s.q_heads + pc.head * group + out_row - t * group;
+      const bool past = start + t >= capacity;  // longer than its page-table row
       float inv = sum == 0.f ? 0.f : 1.f / sum;
       if (past) inv = sum = __uint_as_float(0x7FC00000u);
       uint32_t out[kPer / 2];
@@ -431,13 +588,14 @@ __global__ __launch_bounds__(256, 2) void decode_attention_kernel(KvShape s, KvB
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D + d0);
       #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) dst[i] = out[i];
-      if ((threadIdx.x & 15) == 0) {
+      if (threadIdx.x % kLanes == 0) {
         if (a.lse) a.lse[at] = (big + log2f(sum)) * kLn2;
         if (past) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
       }
     }
-    __syncthreads();  // the shared arrays are free for the next item
-    x0 += whole ? 1 : take;
+    if (k) return;
+    __syncthreads();  // the shared arrays are free for the next piece
+    x0 += pc.take;
   }
 }
 
@@ -453,13 +611,25 @@ hipError_t launch_kv_decode(const KvShape& s, const KvBatch& b, const KvAttentio
   int* counters = static_cast<int*>(workspace);
   float* slots = reinterpret_cast<float*>(counters + kCounterSlots);
   const uint32_t bytes = (uint32_t)(kv_decode_workspace(s) - sizeof(int) * kCounterSlots);
+  // at most this many items, of at most this many units: 32-bit sums for the
+  // common calls, one sequence a lane
+  const int64_t items = ((int64_t)b.tokens * s.group() / kRows + b.n_seqs) * s.kv_heads;
+  const int64_t longest = ((int64_t)s.max_pages << s.page_shift) / kUnit + 2;
+  const bool small = b.n_seqs <= 64 && items * longest < (int64_t)1 << 30;
   const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(kGroups), dim3(256), 0, st, s, b, a, counters, slots, bytes);
+    hipLaunchKernelGGL(kernel, dim3(kGroups), dim3(kThreads), 0, st, s, b, a, counters, slots, bytes);
   };
+  const auto pick = [&](auto d, auto z) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool Z = decltype(z)::value;
+    if (small) go(decode_attention_kernel<D, Z, true>); else go(decode_attention_kernel<D, Z, false>);
+  };
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 128> d128;
   if (s.D == 64) {
-    if (s.zeros) go(decode_attention_kernel<64, true>); else go(decode_attention_kernel<64, false>);
+    if (s.zeros) pick(d64, std::true_type{}); else pick(d64, std::false_type{});
   } else {
-    if (s.zeros) go(decode_attention_kernel<128, true>); else go(decode_attention_kernel<128, false>);
+    if (s.zeros) pick(d128, std::true_type{}); else pick(d128, std::false_type{});
   }
   return hipGetLastError();
 }

@@ -5,10 +5,24 @@
 
 namespace spear {
 
-// Key codes: bf16 bytes of 16 + c.  0x4180 is 16.0; its mantissa's top four
-// bits count units.  even: bits 0-3 of each byte of w, odd: bits 4-7.
-__device__ __forceinline__ uint32_t even16(uint32_t w) { return ((w << 3) & 0x78787878u) | 0x80808080u; }
-__device__ __forceinline__ uint32_t odd16(uint32_t w) { return ((w >> 1) & 0x78787878u) | 0x80808080u; }
+// Codes of a word's low and high half bytes, one a byte.  A byte c below 16 is
+// the 8-bit float (e4m3) of value c 2^-9, normal or not, so that the
+// conversions with a scale of 2^9 give the bf16 or fp16 pair of two codes
+// exactly, and with the sign bit set of their negatives.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return w & 0x0F0F0F0Fu; }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return (w >> 4) & 0x0F0F0F0Fu; }
+__device__ __forceinline__ uint32_t bf16_01(uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.f, false));
+}
+__device__ __forceinline__ uint32_t bf16_23(uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.f, true));
+}
+__device__ __forceinline__ uint32_t f16_01(uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.f, false));
+}
+__device__ __forceinline__ uint32_t f16_23(uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.f, true));
+}
 // fp16 bytes of 64 + c (0x5400 is 64.0; the four bits under its byte count
 // units).
 __device__ __forceinline__ uint32_t even64(uint32_t w) { return (w << 4) & 0xF0F0F0F0u; }
@@ -64,6 +78,48 @@ constexpr float kLn2 = 0.69314718055994530942f;
 __device__ __forceinline__ uint64_t div_u64(uint64_t a, uint64_t b) {
   return ((a | b) >> 32) == 0 ? (uint64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
+
+// Inclusive prefix sum and maximum over the wave's lanes of non-negative
+// 32-bit values: data-parallel-primitive moves within rows of 16 lanes (shifts
+// by 1, 2, 4, 8), then across rows (lane 15 of a row to the next, lane 31 to
+// the upper half).  Lane 63 holds the whole wave's.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_move(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += dpp_move<0x111, 0xF>(v);
+  v += dpp_move<0x112, 0xF>(v);
+  v += dpp_move<0x114, 0xF>(v);
+  v += dpp_move<0x118, 0xF>(v);
+  v += dpp_move<0x142, 0xA>(v);
+  v += dpp_move<0x143, 0xC>(v);
+  return v;
+}
+__device__ __forceinline__ int wave_max(int v) {
+  v = max(v, dpp_move<0x111, 0xF>(v));
+  v = max(v, dpp_move<0x112, 0xF>(v));
+  v = max(v, dpp_move<0x114, 0xF>(v));
+  v = max(v, dpp_move<0x118, 0xF>(v));
+  v = max(v, dpp_move<0x142, 0xA>(v));
+  v = max(v, dpp_move<0x143, 0xC>(v));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// v of the lane and of its partner 16 (32) lanes away, joined by op: the swap
+// of rows leaves both in the two results.
+template <typename F>
+__device__ __forceinline__ float join16(float v, F op) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <typename F>
+__device__ __forceinline__ float join32(float v, F op) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float sum2(float a, float b) { return a + b; }
 
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import SPEAR_EC_ZEROS, _check, _ptr, _stream, load_library
+from .binding import SPEAR_EC_ZEROS, _check, load_library
 
 SPEAR_EC_WS_BAD_PAGE = 2
 
@@ -116,26 +116,43 @@ def spear_ec_kv_workspace_bytes(desc, n_seqs: int, tokens: int) -> int:
     return int(_lib().spear_ec_kv_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(tokens)))
 
 
+def _current_stream(stream, t):
+    """Raw handle of the stream, by default the current one of t's device."""
+    if stream is None:
+        import torch
+        if t.device.type != "cuda":
+            raise ValueError("the tensors must be on the GPU")
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _rows(t, tokens, heads, dim, dtype, name, strided=True):
     """Row stride of a token array, checked against what the call will read or write."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[0] < tokens or t.shape[1] != heads or \
-            t.shape[2] != dim:
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[0] < tokens or shape[1] != heads or \
+            shape[2] != dim:
         raise ValueError(f"{name} must be {dtype} of shape [>= {tokens}, {heads}, {dim}]")
-    st = t.stride()
-    if (st[2] != 1 and dim > 1) or (st[1] != dim and heads > 1) or \
-            (not strided and st[0] != heads * dim and t.shape[0] > 1):
+    row, head, one = t.stride()
+    if shape[0] <= 1:
+        row = heads * dim
+    if one != 1 or (head != dim and heads > 1) or (not strided and row != heads * dim):
         raise ValueError(f"{name}'s rows must be contiguous [{heads}, {dim}]")
-    return st[0] if t.shape[0] > 1 else heads * dim
+    return row
 
 
 def _cache(desc, codes, scales, zeros):
-    c, s, z = kv_cache_shapes(desc)
-    for t, shape, size in ((codes, c, 1), (scales, s, 2), (zeros, z, 1)):
-        if shape is None:
-            continue
-        if t is None or tuple(t.shape) != shape or t.element_size() != size or \
-                not t.is_contiguous():
-            raise ValueError("codes, scales and zeros must have the shapes of kv_cache_shapes(desc)")
+    """Pointers of the cache arrays, checked against the desc."""
+    blocks, D = desc.page_tokens // 16, desc.head_dim
+    pages, heads = desc.pages, desc.kv_heads
+    ok = codes.shape == (pages, heads, blocks, 16 * D) and codes.element_size() == 1 and \
+        codes.is_contiguous() and scales.shape == (pages, heads, blocks, 2, 16) and \
+        scales.element_size() == 2 and scales.is_contiguous()
+    if desc.flags & SPEAR_EC_ZEROS:
+        ok = ok and zeros is not None and zeros.shape == (pages, heads, blocks, 16) and \
+            zeros.element_size() == 1 and zeros.is_contiguous()
+    if not ok:
+        raise ValueError("codes, scales and zeros must have the shapes of kv_cache_shapes(desc)")
+    return codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr()
 
 
 def _table(desc, batch):
@@ -149,25 +166,27 @@ def spear_ec_kv_append(desc, batch, q, k, v, cos_sin, codes, scales, zeros, q_ou
     """Rotate q (to q_out) and k by cos_sin (fp32 [rows, dim], or None) and
     store k and v in the cache; q and q_out may be None."""
     import torch
-    n, D = batch.tokens, desc.head_dim
+    n, D, bf16 = batch.tokens, desc.head_dim, torch.bfloat16
     _table(desc, batch)
-    _cache(desc, codes, scales, zeros)
-    ks = _rows(k, n, desc.kv_heads, D, torch.bfloat16, "k")
-    vs = _rows(v, n, desc.kv_heads, D, torch.bfloat16, "v")
+    cache = _cache(desc, codes, scales, zeros)
+    ks = _rows(k, n, desc.kv_heads, D, bf16, "k")
+    vs = _rows(v, n, desc.kv_heads, D, bf16, "v")
+    qp = op = None
     qs = os = 0
     if q is not None:
-        qs = _rows(q, n, desc.q_heads, D, torch.bfloat16, "q")
+        qs, qp = _rows(q, n, desc.q_heads, D, bf16, "q"), q.data_ptr()
     if q_out is not None:
-        os = _rows(q_out, n, desc.q_heads, D, torch.bfloat16, "q_out")
+        os, op = _rows(q_out, n, desc.q_heads, D, bf16, "q_out"), q_out.data_ptr()
     rope = None
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        shape = cos_sin.shape
+        if cos_sin.dtype is not torch.float32 or len(shape) != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous fp32 [rows, dim]")
-        rope = ctypes.byref(spear_ec_kv_rope(cos_sin.data_ptr(), cos_sin.shape[0],
-                                             cos_sin.shape[1], int(interleaved)))
-    _check(_lib().spear_ec_kv_append(ctypes.byref(desc), ctypes.byref(batch), _ptr(q), qs, _ptr(k),
-                                     ks, _ptr(v), vs, rope, _ptr(codes), _ptr(scales), _ptr(zeros),
-                                     _ptr(q_out), os, _stream(stream)))
+        rope = spear_ec_kv_rope(cos_sin.data_ptr(), shape[0], shape[1], interleaved)
+    status = _lib().spear_ec_kv_append(desc, batch, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, rope,
+                                       *cache, op, os, _current_stream(stream, codes))
+    if status:
+        _check(status)
 
 
 def spear_ec_kv_attention(desc, batch, q, codes, scales, zeros, softmax_scale, out, workspace,
@@ -177,17 +196,22 @@ def spear_ec_kv_attention(desc, batch, q, codes, scales, zeros, softmax_scale, o
     import torch
     n, H, D = batch.tokens, desc.q_heads, desc.head_dim
     _table(desc, batch)
-    _cache(desc, codes, scales, zeros)
+    cache = _cache(desc, codes, scales, zeros)
     qs = _rows(q, n, H, D, torch.bfloat16, "q")
     _rows(out, n, H, D, torch.bfloat16, "out", strided=False)
-    if lse is not None and (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < n or
-                            lse.shape[1] != H or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous fp32 of shape [>= {n}, {H}]")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib().spear_ec_kv_attention(ctypes.byref(desc), ctypes.byref(batch), _ptr(q), qs,
-                                        _ptr(codes), _ptr(scales), _ptr(zeros),
-                                        float(softmax_scale), int(window), _ptr(out), _ptr(lse),
-                                        _ptr(workspace), ws_bytes, _stream(stream)))
+    lp = None
+    if lse is not None:
+        shape = lse.shape
+        if lse.dtype is not torch.float32 or len(shape) != 2 or shape[0] < n or shape[1] != H or \
+                not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous fp32 of shape [>= {n}, {H}]")
+        lp = lse.data_ptr()
+    wp, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
+    status = _lib().spear_ec_kv_attention(desc, batch, q.data_ptr(), qs, *cache, softmax_scale, window,
+                                          out.data_ptr(), lp, wp, ws_bytes,
+                                          _current_stream(stream, codes))
+    if status:
+        _check(status)
 
 
 def spear_ec_kv_dequant_f32(desc, batch, codes, scales, zeros, k_out, v_out, stream=None):
@@ -195,9 +219,10 @@ def spear_ec_kv_dequant_f32(desc, batch, codes, scales, zeros, k_out, v_out, str
     import torch
     n, G, D = batch.tokens, desc.kv_heads, desc.head_dim
     _table(desc, batch)
-    _cache(desc, codes, scales, zeros)
+    cache = _cache(desc, codes, scales, zeros)
     _rows(k_out, n, G, D, torch.float32, "k_out", strided=False)
     _rows(v_out, n, G, D, torch.float32, "v_out", strided=False)
-    _check(_lib().spear_ec_kv_dequant_f32(ctypes.byref(desc), ctypes.byref(batch), _ptr(codes),
-                                          _ptr(scales), _ptr(zeros), _ptr(k_out), _ptr(v_out),
-                                          _stream(stream)))
+    status = _lib().spear_ec_kv_dequant_f32(desc, batch, *cache, k_out.data_ptr(), v_out.data_ptr(),
+                                            _current_stream(stream, codes))
+    if status:
+        _check(status)
