@@ -7,13 +7,14 @@
 // each is cut into `splits` runs of tiles, whose results (O, M, l) the last
 // one to arrive joins in order.
 //
-// A tile.  Every thread loads 16 (head_dim 64: 8) bytes of codes one tile
-// ahead: waves 0-3 a block of keys each, waves 4-7 a block of values, and
-// writes them to LDS as fp16 matrix operands, so that the codes are unpacked
-// once per 256 rows: keys as c - z, exact; values as (c - z) s 2^-e with e
-// the exponent of the block's largest scale, rounded once (2^-11).  Both are
-// laid out in 16-byte chunks whose place is XORed with the row, so that eight
-// consecutive lanes' reads meet different banks.
+// A tile.  Waves 0-3 load a block's codes each (keys and values) one tile
+// ahead and write them to LDS as fp16 matrix operands, so that the codes are
+// unpacked once per item and tile: keys as c - z, exact; values as
+// (c - z) s 2^-e with e the exponent of the block's largest scale, rounded
+// once (2^-11).  Two waves share a SIMD, w and w + 4; the first stages the next
+// tile before its own work on this one, so that its matrix steps meet the
+// other's vector work (staging by all eight after their work: 868 us for
+// prompts of 4096 tokens with 64 heads of 128, so: 802 us).
 //
 // Scores.  S^T = K q^T (32x32x16): a lane holds one row and, with key row
 // bits 2 and 3 exchanged when the tile is written, runs of 8 consecutive
@@ -25,6 +26,7 @@
 // e, so that w = 2^(score + e - M) is at most 1, rounded to fp16 (2^-11); the
 // sum l takes w 2^-e in fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "kv_math.hpp"
@@ -34,44 +36,39 @@ namespace spear {
 namespace {
 
 constexpr int kTileTokens = 64;
-constexpr int kTileRows = 256;
-constexpr int kTileWaves = 8;
 constexpr int kTileTarget = 256;  // workgroups below which items are cut (one per compute unit)
 constexpr int kTileMaxSplits = 16;
+constexpr float kSlack = 8.f;  // M lags the largest score by up to this: w stays below 2^8
 
+// One tile as operands.  Rows are padded by 16 bytes, so that eight
+// consecutive lanes' 16-byte reads meet different banks and every offset is a
+// constant.
 template <int D>
-struct Staged {  // one tile as operands
-  uint16_t k[kTileTokens][D];  // row: token with bits 2 and 3 exchanged
-  uint16_t v[D][kTileTokens];
+struct Staged {
+  uint16_t k[kTileTokens][D + 8];  // row: token with bits 2 and 3 exchanged
+  uint16_t v[D][kTileTokens + 8];
   float ks[kTileTokens];       // key scale times softmax scale and log2 e, over q's power of two
-  int e[4];                    // exponents of the four blocks' value scales
+  float e[4];                  // exponents of the four blocks' value scales
 };
-
-// Byte offsets of 16-byte chunk c of a row.
-template <int D>
-__device__ __forceinline__ int k_chunk(int row, int c) { return row * (2 * D) + ((c ^ (row & 7)) << 4); }
-__device__ __forceinline__ int v_chunk(int d, int c) {
-  return d * (2 * kTileTokens) + ((c ^ ((d ^ (d >> 3)) & 7)) << 4);
-}
 
 // A thread's part of a tile on its way from the cache.
 template <int D>
 struct Fetched {
-  uint32_t w[D / 32];   // codes: of token lane / 4 (keys); of a value column, D / 8 tokens
-  uint32_t ks, kz;      // key scale and zero-point byte of that token
-  u32x4 vs[D / 64];     // value scales of those tokens
-  uint32_t vz[D / 32];  // and zero-point bytes
+  uint32_t k[D / 32], ks, kz;  // token lane / 4: codes, scale, zero-point byte
+  uint32_t v[D / 32];          // codes of a value column, D / 8 tokens
+  u32x4 vs[D / 64];            // value scales of those tokens
+  uint32_t vz[D / 32];         // and zero-point bytes
 };
 
-template <int D, bool ZEROS>
-__global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, KvBatch b,
+template <int D, bool ZEROS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShape s, KvBatch b,
                                                                    KvAttentionArgs a, int splits,
                                                                    int* counters, float* slots) {
   __shared__ int64_t before[kMaxChunks + 1];
   __shared__ __attribute__((aligned(16))) Staged<D> buf[2];
-  __shared__ float red[kTileWaves];
+  __shared__ float red[WAVES];
   __shared__ int flag;
-  constexpr int kRowFloats = D + 2;
+  constexpr int kTileRows = 32 * WAVES, kRowFloats = D + 2;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int n = lane & 31, half = lane >> 5;
   const int capacity = s.max_pages << s.page_shift;
@@ -82,7 +79,7 @@ __global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, Kv
   const auto weight = [&](int i) {
     return (int64_t)load_seq<kTileRows, kTileTokens>(s, b, a.window, i).tiles;
   };
-  if (b.n_seqs > 64) sum_chunks<kTileWaves>(before, b.n_seqs, weight);
+  if (b.n_seqs > 64) sum_chunks<WAVES>(before, b.n_seqs, weight);
   const int head = blockIdx.x % s.kv_heads;
   const int rest = blockIdx.x / s.kv_heads;
   const int split = rest % splits;
@@ -138,7 +135,7 @@ __global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, Kv
   for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
   if (lane == 0) red[wave] = big;
   __syncthreads();
-  for (int i = 0; i < kTileWaves; ++i) big = fmaxf(big, red[i]);
+  for (int i = 0; i < WAVES; ++i) big = fmaxf(big, red[i]);
   const int qe = min(110, max(-110, 15 - __builtin_amdgcn_frexp_expf(big)));  // big 2^qe < 2^15
   const float qmul = __builtin_amdgcn_ldexpf(1.f, qe);
   #pragma unroll
@@ -168,219 +165,257 @@ __global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, Kv
   any_lo = __builtin_amdgcn_readfirstlane(any_lo);
   any_hi = __builtin_amdgcn_readfirstlane(any_hi);
 
-  // ---- staging: wave w fetches block w % 4 of a tile, keys or values
-  const bool is_v = wave >= 4;
+  // ---- staging: waves 0-3 fetch block w of a tile
+  const bool stages = wave < 4;
+  const int part = wave & 3;
   bool bad = false, any_bad = false;
-  // cache block of the wave's part of tile t; positions outside the item's
-  // range stand for the nearest one inside
-  const auto block_of = [&](int t) {
-    const int at = min(max(t * kTileTokens + 16 * (wave & 3), item_lo & ~15), item_hi);
-    const int page = b.page_table[(int64_t)seq * s.max_pages + (at >> s.page_shift)];
-    const bool out = (unsigned)page >= (unsigned)s.pages;
-    const int pb = 1 << (s.page_shift - 4);
-    return out ? -1 : (page * s.kv_heads + head) * pb + ((at >> 4) & (pb - 1));
+  // The wave's part of tile t: positions outside the item's range stand for
+  // the nearest one inside.  The page number is left as loaded until it is
+  // used a tile later (taken for a scalar it would be waited for at once; the
+  // lane's zero keeps the compiler from that).
+  int zero = 0;
+  asm("" : "+v"(zero));
+  const auto place = [&](int t) {
+    return min(max(t * kTileTokens + 16 * part, item_lo & ~15), item_hi);
   };
+  const int* table = b.page_table + (int64_t)seq * s.max_pages;
+  const auto page_of = [&](int t) { return table[(place(t) >> s.page_shift) + zero]; };
+  const auto block_of = [&](int page, int t) {
+    page = __builtin_amdgcn_readfirstlane(page);
+    const int pb = 1 << (s.page_shift - 4);
+    return (unsigned)page < (unsigned)s.pages
+               ? (page * s.kv_heads + head) * pb + ((place(t) >> 4) & (pb - 1)) : -1;
+  };
+  // values, head_dim 64: two lanes a column, eight of its tokens each
+  const int col = D == 128 ? lane : lane >> 1, half_col = D == 128 ? 0 : lane & 1;
   Fetched<D> fe;
   const auto fetch = [&](int blk) {
     bad = blk < 0;
     const int64_t bl = bad ? 0 : blk;
-    const uint8_t* c = a.cache.codes + bl * (16 * D) + (is_v ? 8 * D : 0);
+    const uint8_t* c = a.cache.codes + bl * (16 * D);
     const uint8_t* sc = reinterpret_cast<const uint8_t*>(a.cache.scales) + bl * 64;
-    // values, head_dim 64: two lanes a column, eight of its tokens each
-    const int g = D == 128 ? 0 : lane & 1;
-    if constexpr (D == 128) {
-      const u32x4 w = load16(c + 16 * lane);
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) fe.w[i] = w[i];
-    } else {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(c + 8 * lane);
-      #pragma unroll
-      for (int i = 0; i < 2; ++i) fe.w[i] = w[i];
-    }
-    if (!is_v) {
+    const auto codes = [&](const uint8_t* p, uint32_t (&to)[D / 32]) {
+      if constexpr (D == 128) {
+        const u32x4 w = load16(p + 16 * lane);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = w[i];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p + 8 * lane);
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) to[i] = w[i];
+      }
+    };
+    {
+      codes(c, fe.k);
       fe.ks = *reinterpret_cast<const uint16_t*>(sc + 2 * (lane >> 2));
       if constexpr (ZEROS) fe.kz = a.cache.zeros[bl * 16 + (lane >> 2)];
-    } else {
+    }
+    {
+      codes(c + 8 * D, fe.v);
       #pragma unroll
-      for (int i = 0; i < D / 64; ++i) fe.vs[i] = load16(sc + 32 + 16 * (i + g));
+      for (int i = 0; i < D / 64; ++i) fe.vs[i] = load16(sc + 32 + 16 * (i + half_col) + zero);
       if constexpr (ZEROS) {
-        const uint8_t* zp = a.cache.zeros + bl * 16 + 8 * g;
+        const uint8_t* zp = a.cache.zeros + bl * 16 + 8 * half_col + zero;
         #pragma unroll
         for (int i = 0; i < D / 32; ++i) fe.vz[i] = *reinterpret_cast<const uint32_t*>(zp + 4 * i);
       }
     }
   };
   const auto store = [&](Staged<D>& to, int t) {
-    const int j0 = t * kTileTokens + 16 * (wave & 3);  // the block's first position
-    uint8_t* kp = reinterpret_cast<uint8_t*>(to.k);
-    uint8_t* vp = reinterpret_cast<uint8_t*>(to.v);
-    if (!is_v) {
-      const int token = 16 * (wave & 3) + (lane >> 2), part = lane & 3;
+    const int j0 = t * kTileTokens + 16 * part;  // the block's first position
+    {
+      const int token = 16 * part + (lane >> 2);
       const int r = (token & ~12) | ((token & 4) << 1) | ((token & 8) >> 1);
-      f16x2 z = as_f16x2(0xD480D480u);  // -(64 + 8)
-      if constexpr (ZEROS) {
-        const uint32_t zb = 0xD400u | ((fe.kz & 15u) << 4);
-        z = as_f16x2(zb | (zb << 16));
-      }
+      f16x2 z = as_f16x2(0xC800C800u);  // -8
+      if constexpr (ZEROS) z = as_f16x2(f16_01((fe.kz & 15u) * 0x0101u | 0x8080u));
       #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t e = even64(fe.w[i]), o = odd64(fe.w[i]), top = 0x54545454u;
-        const u32x4 c = {as_u32(as_f16x2(pair01(e, top)) + z), as_u32(as_f16x2(pair23(e, top)) + z),
-                         as_u32(as_f16x2(pair01(o, top)) + z), as_u32(as_f16x2(pair23(o, top)) + z)};
-        *reinterpret_cast<u32x4*>(kp + k_chunk<D>(r, (D / 32) * part + i)) = c;
+        const uint32_t e = low_codes(fe.k[i]), o = high_codes(fe.k[i]);
+        const u32x4 c = {as_u32(as_f16x2(f16_01(e)) + z), as_u32(as_f16x2(f16_23(e)) + z),
+                         as_u32(as_f16x2(f16_01(o)) + z), as_u32(as_f16x2(f16_23(o)) + z)};
+        *reinterpret_cast<u32x4*>(&to.k[r][8 * ((D / 32) * (lane & 3) + i)]) = c;
       }
-      if (part == 0)
+      if ((lane & 3) == 0)
         to.ks[token] = bad ? __uint_as_float(0x7FC00000u) : half_bits_to_f32((uint16_t)fe.ks) * kmul;
-      return;
     }
-    // the lane's value scales; slots that nobody sees count as 0
-    constexpr int kPairs = D / 16;
-    const int g0 = D == 128 ? 0 : lane & 1;
-    uint32_t vs[kPairs];
-    #pragma unroll
-    for (int i = 0; i < kPairs; ++i) vs[i] = fe.vs[i >> 2][i & 3];
-    if (bad || j0 < item_lo || j0 + 15 > item_hi) {
+    {
+      // the lane's value scales; slots that nobody sees count as 0
+      constexpr int kPairs = D / 16;
+      uint32_t vs[kPairs];
       #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const int j = j0 + 8 * g0 + 2 * i;
-        if (bad || j < item_lo || j > item_hi) vs[i] &= 0xFFFF0000u;
-        if (bad || j + 1 < item_lo || j + 1 > item_hi) vs[i] &= 0x0000FFFFu;
+      for (int i = 0; i < kPairs; ++i) vs[i] = fe.vs[i >> 2][i & 3];
+      if (bad || j0 < item_lo || j0 + 15 > item_hi) {
+        #pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const int j = j0 + 8 * half_col + 2 * i;
+          if (bad || j < item_lo || j > item_hi) vs[i] &= 0xFFFF0000u;
+          if (bad || j + 1 < item_lo || j + 1 > item_hi) vs[i] &= 0x0000FFFFu;
+        }
       }
-    }
-    uint32_t mp = vs[0];
-    #pragma unroll
-    for (int i = 1; i < kPairs; ++i) mp = max_pairs(mp, vs[i]);
-    if constexpr (D == 64) mp = max_pairs(mp, (uint32_t)__shfl_xor((int)mp, 1, 64));
-    const float mx = half_bits_to_f32((uint16_t)max(mp & 0xFFFFu, mp >> 16));
-    const int e = mx > 0.f ? __builtin_amdgcn_frexp_expf(mx) : 0;  // every scale < 2^e
-    if (lane == 0) to.e[wave & 3] = e;
-    const int col = D == 128 ? lane : lane >> 1;
-    #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {  // 8 tokens: one chunk of two dimensions
-      const uint32_t w0 = fe.w[2 * i], w1 = fe.w[2 * i + 1], top = 0x54545454u;
-      f16x2 z[4], sg[4];
+      uint32_t mp = vs[0];
       #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f16x2 h = as_f16x2(vs[4 * i + j]);
-        sg[j] = as_f16x2(pack_f16(__builtin_amdgcn_ldexpf((float)h.x, -e),
-                                  __builtin_amdgcn_ldexpf((float)h.y, -e)));
-        z[j] = as_f16x2(0xD480D480u);
+      for (int i = 1; i < kPairs; ++i) mp = max_pairs(mp, vs[i]);
+      if constexpr (D == 64) mp = max_pairs(mp, (uint32_t)__shfl_xor((int)mp, 1, 64));
+      // every scale is below 2^e; at most 2^14, so that 2^-e is an fp16 value
+      const int e = (int)((max(mp & 0xFFFFu, mp >> 16) & 0x7FFFu) >> 10) - 14;
+      const uint32_t unit = pack_f16(__builtin_amdgcn_ldexpf(1.f, -e), __builtin_amdgcn_ldexpf(1.f, -e));
+      if (lane == 0) to.e[part] = (float)e;
+      #pragma unroll
+      for (int i = 0; i < D / 64; ++i) {  // 8 tokens: one chunk of two dimensions
+        f16x2 z[4], sg[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sg[j] = as_f16x2(vs[4 * i + j]) * as_f16x2(unit);
+          z[j] = as_f16x2(0xC800C800u);
+        }
+        if constexpr (ZEROS) {
+          const uint32_t a0 = high_codes(fe.vz[2 * i]) | 0x80808080u;
+          const uint32_t a1 = high_codes(fe.vz[2 * i + 1]) | 0x80808080u;
+          z[0] = as_f16x2(f16_01(a0));
+          z[1] = as_f16x2(f16_23(a0));
+          z[2] = as_f16x2(f16_01(a1));
+          z[3] = as_f16x2(f16_23(a1));
+        }
+        #pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+          const uint32_t w0 = odd ? high_codes(fe.v[2 * i]) : low_codes(fe.v[2 * i]);
+          const uint32_t w1 = odd ? high_codes(fe.v[2 * i + 1]) : low_codes(fe.v[2 * i + 1]);
+          const u32x4 c = {as_u32((as_f16x2(f16_01(w0)) + z[0]) * sg[0]),
+                           as_u32((as_f16x2(f16_23(w0)) + z[1]) * sg[1]),
+                           as_u32((as_f16x2(f16_01(w1)) + z[2]) * sg[2]),
+                           as_u32((as_f16x2(f16_23(w1)) + z[3]) * sg[3])};
+          *reinterpret_cast<u32x4*>(&to.v[2 * col + odd][16 * part + 8 * (i + half_col)]) = c;
+        }
       }
-      if constexpr (ZEROS) {
-        const uint32_t a0 = odd64(fe.vz[2 * i]), a1 = odd64(fe.vz[2 * i + 1]), neg = 0xD4D4D4D4u;
-        z[0] = as_f16x2(pair01(a0, neg));
-        z[1] = as_f16x2(pair23(a0, neg));
-        z[2] = as_f16x2(pair01(a1, neg));
-        z[3] = as_f16x2(pair23(a1, neg));
-      }
-      const uint32_t e0 = even64(w0), e1 = even64(w1), o0 = odd64(w0), o1 = odd64(w1);
-      const u32x4 ev = {as_u32((as_f16x2(pair01(e0, top)) + z[0]) * sg[0]),
-                        as_u32((as_f16x2(pair23(e0, top)) + z[1]) * sg[1]),
-                        as_u32((as_f16x2(pair01(e1, top)) + z[2]) * sg[2]),
-                        as_u32((as_f16x2(pair23(e1, top)) + z[3]) * sg[3])};
-      const u32x4 od = {as_u32((as_f16x2(pair01(o0, top)) + z[0]) * sg[0]),
-                        as_u32((as_f16x2(pair23(o0, top)) + z[1]) * sg[1]),
-                        as_u32((as_f16x2(pair01(o1, top)) + z[2]) * sg[2]),
-                        as_u32((as_f16x2(pair23(o1, top)) + z[3]) * sg[3])};
-      const int chunk = 2 * (wave & 3) + i + g0;
-      *reinterpret_cast<u32x4*>(vp + v_chunk(2 * col, chunk)) = ev;
-      *reinterpret_cast<u32x4*>(vp + v_chunk(2 * col + 1, chunk)) = od;
     }
   };
 
-  float m = -INFINITY, l = 0.f;  // M and the lane's own share of l
+  // M, the lane's own share of l, and O
+  float m = -INFINITY, l = 0.f;
   f32x16 o[D / 32];
   #pragma unroll
   for (int i = 0; i < D / 32; ++i)
     #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
-  if (tb < te) {
-    fetch(block_of(t0 + tb));
-    any_bad |= bad;
-    store(buf[tb & 1], t0 + tb);
-  }
-  for (int ti = tb; ti < te; ++ti) {
-    __syncthreads();
-    const Staged<D>& st = buf[ti & 1];
-    const bool more = ti + 1 < te;
-    if (more) fetch(block_of(t0 + ti + 1));
+  f32x16 sc[2];  // scores of a tile
+  u32x4 pf[4];   // and its probabilities, the operands of its values
+  const auto seen = [&](int ti) {
     const int j0 = (t0 + ti) * kTileTokens;
-    if (j0 <= any_hi && j0 + kTileTokens - 1 >= any_lo) {
-      const uint8_t* kp = reinterpret_cast<const uint8_t*>(st.k);
-      const uint8_t* vp = reinterpret_cast<const uint8_t*>(st.v);
-      f32x16 sc[2];
+    return j0 <= any_hi && j0 + kTileTokens - 1 >= any_lo;
+  };
+  const auto scores = [&](const Staged<D>& st) {
+    #pragma unroll
+    for (int r = 0; r < 16; ++r) sc[0][r] = sc[1][r] = 0.f;
+    #pragma unroll
+    for (int i = 0; i < D / 16; ++i)
       #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        #pragma unroll
-        for (int r = 0; r < 16; ++r) sc[t][r] = 0.f;
-        #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(kp + k_chunk<D>(32 * t + n, 2 * i + half));
-          sc[t] = mfma32x32x16_f16(kf, qf[i], sc[t]);
-        }
+        const u32x4 kf = *reinterpret_cast<const u32x4*>(&st.k[32 * t + n][16 * i + 8 * half]);
+        sc[t] = mfma32x32x16_f16(kf, qf[i], sc[t]);
       }
-      // lane's tokens: 16 g + 8 half + 0 .. 7 for g = 0 .. 3
-      float top[4];
+    // reads four operands ahead of the matrix steps
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+    #pragma unroll
+    for (int i = 0; i < D / 8 - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+  };
+  const auto softmax = [&](const Staged<D>& st, int j0) {
+    // lane's tokens: 16 g + 8 half + 0 .. 7 for g = 0 .. 3
+    #pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 k0 = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half]);
+      const f32x4 k1 = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half + 4]);
       #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 k0 = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half]);
-        const f32x4 k1 = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half + 4]);
-        #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          sc[g >> 1][8 * (g & 1) + r] *= r < 4 ? k0[r & 3] : k1[r & 3];
-      }
-      if (j0 < all_lo || j0 + kTileTokens - 1 > all_hi) {
-        #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int j = j0 + 16 * g + 8 * half + r;
-            if (j < lo || j > hi) sc[g >> 1][8 * (g & 1) + r] = -INFINITY;
-          }
-      }
-      float mn = m;
-      float eb[4];
-      #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        eb[g] = (float)st.e[g];
-        top[g] = sc[g >> 1][8 * (g & 1)];
-        #pragma unroll
-        for (int r = 1; r < 8; ++r) top[g] = fmaxf(top[g], sc[g >> 1][8 * (g & 1) + r]);
-        mn = fmaxf(mn, top[g] + eb[g]);
-      }
-      mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
-      if (__any(mn > m)) {
-        const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
-        l *= alpha;
-        #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] *= alpha;
-        m = mn;
-      }
-      u32x4 pf[4];
-      #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float ref = m == -INFINITY ? 0.f : m - eb[g];
-        float sum = 0.f;
-        #pragma unroll
-        for (int r = 0; r < 8; r += 2) {
-          const float w0 = fast_exp2(sc[g >> 1][8 * (g & 1) + r] - ref);
-          const float w1 = fast_exp2(sc[g >> 1][8 * (g & 1) + r + 1] - ref);
-          sum += w0 + w1;
-          pf[g][r >> 1] = pack_f16(w0, w1);
-        }
-        l += __builtin_amdgcn_ldexpf(sum, -st.e[g]);
-      }
+      for (int r = 0; r < 8; ++r)
+        sc[g >> 1][8 * (g & 1) + r] *= r < 4 ? k0[r & 3] : k1[r & 3];
+    }
+    if (j0 < all_lo || j0 + kTileTokens - 1 > all_hi) {
       #pragma unroll
       for (int g = 0; g < 4; ++g)
         #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const u32x4 vf = *reinterpret_cast<const u32x4*>(vp + v_chunk(32 * i + n, 2 * g + half));
-          o[i] = mfma32x32x16_f16(vf, pf[g], o[i]);
+        for (int r = 0; r < 8; ++r) {
+          const int j = j0 + 16 * g + 8 * half + r;
+          if (j < lo || j > hi) sc[g >> 1][8 * (g & 1) + r] = -INFINITY;
         }
     }
-    if (more) {
+    const f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
+    float mn = m;
+    #pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float top = sc[g >> 1][8 * (g & 1)];
+      #pragma unroll
+      for (int r = 1; r < 8; ++r) top = fmaxf(top, sc[g >> 1][8 * (g & 1) + r]);
+      mn = fmaxf(mn, top + eb[g]);
+    }
+    mn = join32(mn, larger);
+    if (__any(mn > m + kSlack)) {
+      const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
+      l *= alpha;
+      #pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] *= alpha;
+      m = mn;
+    }
+    #pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float ref = m == -INFINITY ? 0.f : m - eb[g];
+      float sum = 0.f;
+      #pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        const float w0 = fast_exp2(sc[g >> 1][8 * (g & 1) + r] - ref);
+        const float w1 = fast_exp2(sc[g >> 1][8 * (g & 1) + r + 1] - ref);
+        sum += w0 + w1;
+        pf[g][r >> 1] = pack_f16(w0, w1);
+      }
+      l += __builtin_amdgcn_ldexpf(sum, -(int)eb[g]);
+    }
+  };
+  const auto values = [&](const Staged<D>& st) {
+    #pragma unroll
+    for (int g = 0; g < 4; ++g)
+      #pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const u32x4 vf = *reinterpret_cast<const u32x4*>(&st.v[32 * i + n][16 * g + 8 * half]);
+        o[i] = mfma32x32x16_f16(vf, pf[g], o[i]);
+      }
+  };
+  // What the waves hand each other lies in LDS: nothing else is waited for.
+  const auto meet = [&] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  };
+  // Tiles reach LDS by way of registers: the one fetched (tile `got`) is
+  // stored a tile ahead of its use, then the next is fetched.
+  int page = 0;  // page of the wave's part of the tile after the one fetched
+  const auto begin = [&](int ti) {
+    fetch(block_of(page_of(t0 + ti), t0 + ti));
+    any_bad |= bad;
+    if (ti + 1 < te) page = page_of(t0 + ti + 1);
+  };
+  const auto advance = [&](int ti) {  // store tile ti, fetch tile ti + 1
+    store(buf[ti & 1], t0 + ti);
+    if (ti + 1 < te) {
+      fetch(block_of(page, t0 + ti + 1));
       any_bad |= bad;
-      store(buf[(ti + 1) & 1], t0 + ti + 1);
+      if (ti + 2 < te) page = page_of(t0 + ti + 2);
+    }
+  };
+  if (tb < te) {
+    if (stages) {
+      begin(tb);
+      advance(tb);
+    }
+    for (int ti = tb; ti < te; ++ti) {
+      meet();
+      if (stages && ti + 1 < te) advance(ti + 1);
+      if (seen(ti)) {
+        scores(buf[ti & 1]);
+        softmax(buf[ti & 1], (t0 + ti) * kTileTokens);
+        values(buf[ti & 1]);
+      }
     }
   }
   l += __shfl_xor(l, 32, 64);
@@ -396,7 +431,7 @@ __global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, Kv
       return make_rsrc(slots + (item * splits + sp) * (kRowFloats * kTileRows), bytes);
     };
     const uint32_t me = (wave * 32 + n) * 4;
-    {
+    if (live) {
       const rsrc_t rs = slot(split);
       #pragma unroll
       for (int i = 0; i < D / 32; ++i)
@@ -418,7 +453,7 @@ __global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, Kv
     }
     __syncthreads();
     last = flag != 0;
-    if (last) {
+    if (last && live) {
       float big_m = -INFINITY;
       for (int sp = 0; sp < splits; ++sp) big_m = fmaxf(big_m, bload_dev(slot(sp), D * (kTileRows * 4) + me, 0));
       l = 0.f;
@@ -461,37 +496,50 @@ __global__ __launch_bounds__(512, 2) void prefill_attention_kernel(KvShape s, Kv
   }
 }
 
-// Items of a call are at most this many (their number is device data).
-int64_t item_bound(const KvShape& s, int n_seqs, int tokens) {
-  const int64_t rows = (int64_t)tokens * s.group();
-  return (rows / kTileRows + std::min(n_seqs, tokens)) * s.kv_heads;
+// A call's rows are taken 256 at a time, or 128 where its sequences have no
+// more on average.
+bool narrow(const KvShape& s, int n_seqs, int tokens) {
+  return (int64_t)tokens * s.group() <= (int64_t)128 * n_seqs;
 }
 
-int split_count(const KvShape& s, int n_seqs, int tokens) {
-  const int64_t items = std::max<int64_t>(1, item_bound(s, n_seqs, tokens));
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kTileMaxSplits, (kTileTarget + items - 1) / items));
+// Items of a call are at most this many (their number is device data).
+int64_t item_bound(const KvShape& s, int n_seqs, int tokens, int tile_rows) {
+  const int64_t rows = (int64_t)tokens * s.group();
+  return (rows / tile_rows + std::min(n_seqs, tokens)) * s.kv_heads;
 }
 
 }  // namespace
 
 size_t kv_prefill_workspace(const KvShape& s) {
-  // split_count(items) * items < kTileTarget + items <= 2 * kTileTarget where items are cut
-  return sizeof(int) * kCounterSlots + sizeof(float) * 2 * kTileTarget * kTileRows * (s.D + 2);
+  // items are cut below `target` workgroups, target being as many as fit on
+  // the chip: fewer than 2 target pieces of 256 rows, or of 128 and twice as many
+  return sizeof(int) * kCounterSlots + sizeof(float) * 2 * kTileTarget * 256 * (s.D + 2);
 }
 
 hipError_t launch_kv_prefill(const KvShape& s, const KvBatch& b, const KvAttentionArgs& a,
                              void* workspace, hipStream_t st) {
   int* counters = static_cast<int*>(workspace);
   float* slots = reinterpret_cast<float*>(counters + kCounterSlots);
-  const int splits = split_count(s, b.n_seqs, b.tokens);
-  const int64_t wgs = item_bound(s, b.n_seqs, b.tokens) * splits;
-  const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(512), 0, st, s, b, a, splits, counters, slots);
+  const auto go = [&](auto d, auto z, auto w) {
+    constexpr int D = decltype(d)::value, W = decltype(w)::value;
+    const int64_t target = kTileTarget * (8 / W);
+    const int64_t items = std::max<int64_t>(1, item_bound(s, b.n_seqs, b.tokens, 32 * W));
+    const int splits =
+        (int)std::max<int64_t>(1, std::min<int64_t>(kTileMaxSplits, (target + items - 1) / items));
+    hipLaunchKernelGGL((prefill_attention_kernel<D, decltype(z)::value, W>),
+                       dim3((unsigned)(items * splits)), dim3(64 * W), 0, st, s, b, a, splits, counters,
+                       slots);
   };
+  const auto pick = [&](auto d, auto z) {
+    if (narrow(s, b.n_seqs, b.tokens)) go(d, z, std::integral_constant<int, 4>{});
+    else go(d, z, std::integral_constant<int, 8>{});
+  };
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 128> d128;
   if (s.D == 64) {
-    if (s.zeros) go(prefill_attention_kernel<64, true>); else go(prefill_attention_kernel<64, false>);
+    if (s.zeros) pick(d64, std::true_type{}); else pick(d64, std::false_type{});
   } else {
-    if (s.zeros) go(prefill_attention_kernel<128, true>); else go(prefill_attention_kernel<128, false>);
+    if (s.zeros) pick(d128, std::true_type{}); else pick(d128, std::false_type{});
   }
   return hipGetLastError();
 }
