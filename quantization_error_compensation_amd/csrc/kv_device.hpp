@@ -14,32 +14,35 @@ struct KvRow {
 };
 
 // Row t's sequence: the number of offsets at or below t, counted by the whole
-// wave (64 offsets a step), so the search costs one memory round trip for up
-// to 64 sequences.  Offsets that do not ascend can only yield "none" or a
-// row inside the sequence it names.  Wave-uniform t; every lane takes part.
+// wave (64 offsets a step), so that the search costs one memory round trip for
+// up to 63 sequences; their lengths come along with it.  Offsets that do not
+// ascend can only yield "none" or a row inside the sequence it names.
+// Wave-uniform t; every lane takes part.
 __device__ __forceinline__ KvRow kv_row(const KvBatch& b, int t) {
-  KvRow r{-1, -1};
-  if (!b.q_offsets) {
-    r.seq = t;  // tokens == n_seqs
-    r.pos = max(__builtin_amdgcn_readfirstlane(b.seq_lens[t]), 0) - 1;
-    return r;
-  }
   const int lane = threadIdx.x & 63;
-  int below = 0;  // offsets <= t
-  for (int i = 0; i <= b.n_seqs; i += 64) {
-    const bool le = i + lane <= b.n_seqs && b.q_offsets[i + lane] <= t;
-    const int c = __popcll(__ballot(le));
-    below += c;
-    if (c < 64) break;
+  if (!b.q_offsets)  // tokens == n_seqs
+    return KvRow{t, max(__builtin_amdgcn_readfirstlane(b.seq_lens[t]), 0) - 1};
+  const int off = b.q_offsets[min(lane, b.n_seqs)];
+  const int len = b.seq_lens[min(lane, b.n_seqs - 1)];
+  int below = __popcll(__ballot(lane <= b.n_seqs && off <= t));
+  for (int c = 64; c <= b.n_seqs && below == c; c += 64) {
+    const int o = b.q_offsets[min(c + lane, b.n_seqs)];
+    below += __popcll(__ballot(c + lane <= b.n_seqs && o <= t));
   }
   const int s = below - 1;
-  if (s < 0 || s >= b.n_seqs) return r;
-  const int first = __builtin_amdgcn_readfirstlane(b.q_offsets[s]);
-  const int end = __builtin_amdgcn_readfirstlane(b.q_offsets[s + 1]);
-  if (t < first || t >= end) return r;
-  r.seq = s;
-  r.pos = max(__builtin_amdgcn_readfirstlane(b.seq_lens[s]), 0) - (end - t);
-  return r;
+  if (s < 0 || s >= b.n_seqs) return KvRow{-1, -1};
+  int first, end, n;
+  if (s < 63) {
+    first = __builtin_amdgcn_readlane(off, s);
+    end = __builtin_amdgcn_readlane(off, s + 1);
+    n = __builtin_amdgcn_readlane(len, s);
+  } else {
+    first = __builtin_amdgcn_readfirstlane(b.q_offsets[s]);
+    end = __builtin_amdgcn_readfirstlane(b.q_offsets[s + 1]);
+    n = __builtin_amdgcn_readfirstlane(b.seq_lens[s]);
+  }
+  if (t < first || t >= min(end, b.tokens)) return KvRow{-1, -1};
+  return KvRow{s, max(n, 0) - (end - t)};
 }
 
 // Index of a (page, head)'s 16-token block in the cache, -1 for a position

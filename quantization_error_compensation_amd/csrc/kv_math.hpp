@@ -157,6 +157,27 @@ __device__ __forceinline__ Seq load_seq(const KvShape& s, const KvBatch& b, int 
   return q;
 }
 
+// For up to 64 sequences, one a lane with its work w (32-bit sums): the lane
+// whose work holds x, -1 past the end, and the work before it.
+__device__ __forceinline__ int lane_of(int w, int x, int& base) {
+  const int upto = wave_prefix(w);
+  const uint64_t above = __ballot(upto > x);
+  if (!above) return -1;
+  const int who = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)above) - 1);
+  base = __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(w, who);
+  return who;
+}
+__device__ __forceinline__ Seq seq_of_lane(const Seq& own, int who) {
+  Seq q;
+  q.first = __builtin_amdgcn_readlane(own.first, who);
+  q.n = __builtin_amdgcn_readlane(own.n, who);
+  q.len = __builtin_amdgcn_readlane(own.len, who);
+  q.tiles = __builtin_amdgcn_readlane(own.tiles, who);
+  q.u0 = __builtin_amdgcn_readlane(own.u0, who);
+  q.nb = __builtin_amdgcn_readlane(own.nb, who);
+  return q;
+}
+
 // Work of the sequences before each 64 of them, and where a piece of work
 // lies: every workgroup adds the lengths up itself, since they are device
 // data.
