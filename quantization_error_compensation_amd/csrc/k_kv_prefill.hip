@@ -4,7 +4,7 @@
 // Work.  An item is 256 rows (token, query head) of a sequence that read one
 // kv head; its eight waves hold 32 rows each, and walk the tokens that the
 // item sees in tiles of 64.  Where the items alone leave compute units idle
-// each is cut into `splits` runs of tiles, whose results (O, M, l) the last
+// each is cut into runs of tiles, whose results (O, M, l) the last
 // one to arrive joins in order.
 //
 // A tile.  Waves 0-3 load a block's codes each (keys and values) one tile
@@ -14,7 +14,12 @@
 // once (2^-11).  Two waves share a SIMD, w and w + 4; the first stages the next
 // tile before its own work on this one, so that its matrix steps meet the
 // other's vector work (staging by all eight after their work: 868 us for
-// prompts of 4096 tokens with 64 heads of 128, so: 802 us).
+// prompts of 4096 tokens with 64 heads of 128, so: 802 us).  Items of 128 rows
+// leave the staging to waves 0-3 alone, two tiles ahead, and the rows to waves
+// 4-7: such calls read the cache more often per row, and waited for it (8 chats
+// of 72 rows behind 4096 tokens: two workgroups of four waves a compute unit
+// 45 us, this one 42, with the cut by the items that there are and all waves
+// joining 35).
 //
 // Scores.  S^T = K q^T (32x32x16): a lane holds one row and, with key row
 // bits 2 and 3 exchanged when the tile is written, runs of 8 consecutive
@@ -22,11 +27,24 @@
 // fp16 times one power of two for the item's rows (its largest element below
 // 2^15): bf16 has 8 significant bits and fp16 eleven, so an element is exact
 // unless it is below 2^-29 of the largest, and then off by at most 2^-39 of
-// it.  The running reference M of a row is the largest score plus its block's
-// e, so that w = 2^(score + e - M) is at most 1, rounded to fp16 (2^-11); the
-// sum l takes w 2^-e in fp32.
+// it.  A row's probabilities are w = 2^(score + e - M), rounded to fp16
+// (2^-11); the sum l takes w 2^-e in fp32.  The reference M is the largest
+// score plus its block's e up to some tile and stays there until a lane's
+// eight w add up to more than 2^14 (fp16 holds up to 2^16), so most tiles
+// need no maximum: their w are taken at once, and again, against a new M,
+// where the sum says so (a maximum per tile: 801 and 164 us for prompts of
+// 4096 and a chunk of 512 tokens, so: 789 and 159 us).
+//
+// Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
+// steps and takes about 4600: some 3000 of vector work (two thirds of it the
+// softmax, the rest unpacking) and 2300 of LDS reads run beside them, and two
+// waves a SIMD, all that 230 registers leave room for, do not overlap them
+// further.  Computing a tile's scores beside the previous tile's softmax in
+// one wave, with eight or four waves a workgroup, took 1.09 to 1.2 times as
+// long; wave priorities changed nothing.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "internal.hpp"
 #include "kv_math.hpp"
@@ -37,8 +55,11 @@ namespace {
 
 constexpr int kTileTokens = 64;
 constexpr int kTileTarget = 256;  // workgroups below which items are cut (one per compute unit)
-constexpr int kTileMaxSplits = 16;
-constexpr float kSlack = 8.f;  // M lags the largest score by up to this: w stays below 2^8
+constexpr int kTileMaxSplits = 32;
+constexpr int kMinTiles = 4;      // a cut item's runs have at least as many tiles
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr float kNever = -3e38f;  // M before any score: below any, and finite
+constexpr float kMostSum = 0x1p14f;  // of a lane's eight weights: above it M is raised
 
 // One tile as operands.  Rows are padded by 16 bytes, so that eight
 // consecutive lanes' 16-byte reads meet different banks and every offset is a
@@ -58,17 +79,19 @@ struct Fetched {
   uint32_t v[D / 32];          // codes of a value column, D / 8 tokens
   u32x4 vs[D / 64];            // value scales of those tokens
   uint32_t vz[D / 32];         // and zero-point bytes
+  bool bad;                    // the block lies on a page outside the cache
+  int page;                    // page of the wave's part of the tile fetched next
 };
 
-template <int D, bool ZEROS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShape s, KvBatch b,
-                                                                   KvAttentionArgs a, int splits,
+template <int D, bool ZEROS, bool NARROW, bool SMALL>
+__global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape s, KvBatch b,
+                                                                   KvAttentionArgs a,
                                                                    int* counters, float* slots) {
-  __shared__ int64_t before[kMaxChunks + 1];
+  __shared__ int64_t before[SMALL ? 1 : kMaxChunks + 1];
   __shared__ __attribute__((aligned(16))) Staged<D> buf[2];
-  __shared__ float red[WAVES];
+  __shared__ float red[kWaves];
   __shared__ int flag;
-  constexpr int kTileRows = 32 * WAVES, kRowFloats = D + 2;
+  constexpr int kTileRows = NARROW ? 128 : 256, kRowFloats = D + 2;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int n = lane & 31, half = lane >> 5;
   const int capacity = s.max_pages << s.page_shift;
@@ -76,25 +99,35 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
 
   // ---- the item: heads fastest (one head's items on one XCD), a sequence's
   // last rows first (they see the most tokens)
-  const auto weight = [&](int i) {
-    return (int64_t)load_seq<kTileRows, kTileTokens>(s, b, a.window, i).tiles;
-  };
-  if (b.n_seqs > 64) sum_chunks<WAVES>(before, b.n_seqs, weight);
   const int head = blockIdx.x % s.kv_heads;
   const int rest = blockIdx.x / s.kv_heads;
-  const int split = rest % splits;
-  const int64_t x = rest / splits;
-  int64_t total;
-  if (b.n_seqs > 64) {
-    total = before[(b.n_seqs + 63) / 64];
+  const auto seq_at = [&](int i) { return load_seq<kTileRows, kTileTokens>(s, b, a.window, i); };
+  const auto cuts = [&](int tiles) {  // runs an item is cut into
+    const int items = tiles * s.kv_heads;
+    return items ? min(kTileMaxSplits, (kTileTarget + items - 1) / items) : 1;
+  };
+  int seq, seq_base, splits;
+  Seq q;
+  if constexpr (SMALL) {
+    Seq own{0, 0, 0, 0, 0, 1};
+    if (lane < b.n_seqs) own = seq_at(lane);
+    splits = cuts(__builtin_amdgcn_readlane(wave_prefix(own.tiles), 63));
+    seq = lane_of(own.tiles, rest / splits, seq_base);
+    if (seq < 0) return;
+    q = seq_of_lane(own, seq);
   } else {
-    total = wave_sum(lane < b.n_seqs ? weight(lane) : (int64_t)0);
+    const auto weight = [&](int i) { return (int64_t)seq_at(i).tiles; };
+    sum_chunks<kWaves>(before, b.n_seqs, weight);
+    const int tiles = (int)before[(b.n_seqs + 63) / 64];
+    splits = cuts(tiles);
+    if (rest / splits >= tiles) return;
+    int64_t base;
+    seq = find_seq(before, b.n_seqs, rest / splits, weight, base);
+    seq_base = (int)base;
+    q = seq_at(seq);
   }
-  if (x >= total) return;
-  int64_t seq_base;
-  const int seq = __builtin_amdgcn_readfirstlane(find_seq(before, b.n_seqs, x, weight, seq_base));
-  const Seq q = load_seq<kTileRows, kTileTokens>(s, b, a.window, seq);
-  const int tile = q.tiles - 1 - (int)(x - seq_base);
+  const int x = rest / splits, split = rest - x * splits;
+  const int tile = q.tiles - 1 - (x - seq_base);
   const int rows_n = q.n * group;
 
   // ---- tokens that the item's rows see
@@ -105,16 +138,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
   const int item_lo = a.window ? max(0, min(pos0, capacity - 1) - a.window + 1) : 0;
   const int t0 = item_lo / kTileTokens;
   const int nt = item_hi < 0 ? 0 : item_hi / kTileTokens - t0 + 1;
-  const int per = (nt + splits - 1) / splits;
+  // runs of at least kMinTiles tiles: short items are cut less, or not at all
+  const int per = max((nt + splits - 1) / splits, kMinTiles);
+  const int parts = max(1, (nt + per - 1) / per);
+  if (split >= parts) return;
   const int tb = min(nt, split * per), te = min(nt, tb + per);
 
   // ---- the lane's query row
-  const int row = row0 + wave * 32 + n;
-  const bool live = row < rows_n;
+  const int row = row0 + (NARROW ? wave - 4 : wave) * 32 + n;
+  const bool live = row < rows_n && (!NARROW || wave >= 4);
   const int tok = live ? row / group : 0;
   const int qh = head * group + (live ? row - tok * group : 0);
   const int pos = live ? start + tok : -1;
-  const int hi = min(pos, capacity - 1);
+  const int hi = live ? min(pos, capacity - 1) : 0x7FFFFFFF;  // no row: nothing to mask
   const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
   u32x4 qf[D / 16];
   float big = 0.f;
@@ -135,7 +171,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
   for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
   if (lane == 0) red[wave] = big;
   __syncthreads();
-  for (int i = 0; i < WAVES; ++i) big = fmaxf(big, red[i]);
+  for (int i = 0; i < kWaves; ++i) big = fmaxf(big, red[i]);
   const int qe = min(110, max(-110, 15 - __builtin_amdgcn_frexp_expf(big)));  // big 2^qe < 2^15
   const float qmul = __builtin_amdgcn_ldexpf(1.f, qe);
   #pragma unroll
@@ -151,7 +187,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
     }
   }
   const float kmul = a.scale * kLog2e * __builtin_amdgcn_ldexpf(1.f, -qe);
-  int all_lo = live ? lo : 0, all_hi = live ? hi : 0x7FFFFFFF;
+  int all_lo = lo, all_hi = hi;
   int any_lo = live && hi >= lo ? lo : 0x7FFFFFFF, any_hi = live ? hi : -1;
   #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -168,7 +204,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
   // ---- staging: waves 0-3 fetch block w of a tile
   const bool stages = wave < 4;
   const int part = wave & 3;
-  bool bad = false, any_bad = false;
+  bool any_bad = false;
   // The wave's part of tile t: positions outside the item's range stand for
   // the nearest one inside.  The page number is left as loaded until it is
   // used a tile later (taken for a scalar it would be waited for at once; the
@@ -188,9 +224,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
   };
   // values, head_dim 64: two lanes a column, eight of its tokens each
   const int col = D == 128 ? lane : lane >> 1, half_col = D == 128 ? 0 : lane & 1;
-  Fetched<D> fe;
-  const auto fetch = [&](int blk) {
-    bad = blk < 0;
+  const auto fetch = [&](Fetched<D>& fe, int blk) {
+    const bool bad = fe.bad = blk < 0;
+    any_bad |= bad;
     const int64_t bl = bad ? 0 : blk;
     const uint8_t* c = a.cache.codes + bl * (16 * D);
     const uint8_t* sc = reinterpret_cast<const uint8_t*>(a.cache.scales) + bl * 64;
@@ -221,7 +257,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
       }
     }
   };
-  const auto store = [&](Staged<D>& to, int t) {
+  const auto store = [&](Staged<D>& to, const Fetched<D>& fe, int t) {
+    const bool bad = fe.bad;
     const int j0 = t * kTileTokens + 16 * part;  // the block's first position
     {
       const int token = 16 * part + (lane >> 2);
@@ -291,7 +328,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
   };
 
   // M, the lane's own share of l, and O
-  float m = -INFINITY, l = 0.f;
+  float m = kNever, l = 0.f;
   f32x16 o[D / 32];
   #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -322,55 +359,74 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
     }
     __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
   };
-  const auto softmax = [&](const Staged<D>& st, int j0) {
-    // lane's tokens: 16 g + 8 half + 0 .. 7 for g = 0 .. 3
+  // The lane's tokens of a tile: 16 g + 8 half + 0 .. 7 for g = 0 .. 3.
+  const auto key_scale = [&](const Staged<D>& st, int g, f32x4 (&k)[2]) {
+    k[0] = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half]);
+    k[1] = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half + 4]);
+  };
+  const auto hidden = [&](int j0, int g, int r) {
+    const int j = j0 + 16 * g + 8 * half + r;
+    return j < lo || j > hi;
+  };
+  // Probabilities against M as it is, and their sums by group.
+  const auto weights = [&](auto edge, const Staged<D>& st, f32x4 eb, int j0, f32x4& sums) {
     #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const f32x4 k0 = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half]);
-      const f32x4 k1 = *reinterpret_cast<const f32x4*>(&st.ks[16 * g + 8 * half + 4]);
-      #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        sc[g >> 1][8 * (g & 1) + r] *= r < 4 ? k0[r & 3] : k1[r & 3];
-    }
-    if (j0 < all_lo || j0 + kTileTokens - 1 > all_hi) {
-      #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int j = j0 + 16 * g + 8 * half + r;
-          if (j < lo || j > hi) sc[g >> 1][8 * (g & 1) + r] = -INFINITY;
-        }
-    }
-    const f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
-    float mn = m;
-    #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float top = sc[g >> 1][8 * (g & 1)];
-      #pragma unroll
-      for (int r = 1; r < 8; ++r) top = fmaxf(top, sc[g >> 1][8 * (g & 1) + r]);
-      mn = fmaxf(mn, top + eb[g]);
-    }
-    mn = join32(mn, larger);
-    if (__any(mn > m + kSlack)) {
-      const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
-      l *= alpha;
-      #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] *= alpha;
-      m = mn;
-    }
-    #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float ref = m == -INFINITY ? 0.f : m - eb[g];
+      const float ref = m - eb[g];
+      f32x4 k[2];
+      key_scale(st, g, k);
       float sum = 0.f;
       #pragma unroll
       for (int r = 0; r < 8; r += 2) {
-        const float w0 = fast_exp2(sc[g >> 1][8 * (g & 1) + r] - ref);
-        const float w1 = fast_exp2(sc[g >> 1][8 * (g & 1) + r + 1] - ref);
+        const int at = 8 * (g & 1) + r;
+        float w0 = fast_exp2(fmaf(sc[g >> 1][at], k[r >> 2][r & 3], -ref));
+        float w1 = fast_exp2(fmaf(sc[g >> 1][at + 1], k[r >> 2][(r & 3) + 1], -ref));
+        if constexpr (decltype(edge)::value) {
+          if (hidden(j0, g, r)) w0 = 0.f;
+          if (hidden(j0, g, r + 1)) w1 = 0.f;
+        }
         sum += w0 + w1;
         pf[g][r >> 1] = pack_f16(w0, w1);
       }
-      l += __builtin_amdgcn_ldexpf(sum, -(int)eb[g]);
+      sums[g] = sum;
     }
+  };
+  // M becomes the largest score so far (plus e).
+  const auto raise = [&](const Staged<D>& st, f32x4 eb, int j0) {
+    float mn = m;
+    #pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f32x4 k[2];
+      key_scale(st, g, k);
+      #pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float x = fmaf(sc[g >> 1][8 * (g & 1) + r], k[r >> 2][r & 3], eb[g]);
+        if (!hidden(j0, g, r)) mn = fmaxf(mn, x);
+      }
+    }
+    mn = join32(mn, larger);
+    const float alpha = fast_exp2(m - mn);
+    l *= alpha;
+    #pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= alpha;
+    m = mn;
+  };
+  const auto softmax = [&](const Staged<D>& st, int j0) {
+    const f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
+    const bool edge = j0 < all_lo || j0 + kTileTokens - 1 > all_hi;
+    f32x4 sums;
+    bool done = false;
+    if (!edge) {
+      weights(std::false_type{}, st, eb, j0, sums);
+      const float most = fmaxf(fmaxf(sums[0], sums[1]), fmaxf(sums[2], sums[3]));
+      done = !__any(most > kMostSum);
+    }
+    if (!done) {
+      raise(st, eb, j0);
+      weights(std::true_type{}, st, eb, j0, sums);
+    }
+    #pragma unroll
+    for (int g = 0; g < 4; ++g) l += __builtin_amdgcn_ldexpf(sums[g], -(int)eb[g]);
   };
   const auto values = [&](const Staged<D>& st) {
     #pragma unroll
@@ -387,119 +443,184 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prefill_attention_kernel(KvShap
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
-  // Tiles reach LDS by way of registers: the one fetched (tile `got`) is
-  // stored a tile ahead of its use, then the next is fetched.
-  int page = 0;  // page of the wave's part of the tile after the one fetched
-  const auto begin = [&](int ti) {
-    fetch(block_of(page_of(t0 + ti), t0 + ti));
-    any_bad |= bad;
-    if (ti + 1 < te) page = page_of(t0 + ti + 1);
+  // Tiles reach LDS by way of registers: the one that lies in f, `ti`, is
+  // stored a tile ahead of its use, then the one kAhead later fetched into f.
+  constexpr int kAhead = NARROW ? 2 : 1;
+  const auto fetch_tile = [&](Fetched<D>& f, int ti) {
+    if (ti < te) fetch(f, block_of(f.page, t0 + ti));
+    if (ti + kAhead < te) f.page = page_of(t0 + ti + kAhead);
   };
-  const auto advance = [&](int ti) {  // store tile ti, fetch tile ti + 1
-    store(buf[ti & 1], t0 + ti);
-    if (ti + 1 < te) {
-      fetch(block_of(page, t0 + ti + 1));
-      any_bad |= bad;
-      if (ti + 2 < te) page = page_of(t0 + ti + 2);
-    }
+  const auto advance = [&](Fetched<D>& f, int ti) {
+    if (ti >= te) return;
+    store(buf[ti & 1], f, t0 + ti);
+    fetch_tile(f, ti + kAhead);
+  };
+  const auto attend = [&](int ti) {
+    if (!seen(ti)) return;
+    scores(buf[ti & 1]);
+    softmax(buf[ti & 1], (t0 + ti) * kTileTokens);
+    values(buf[ti & 1]);
   };
   if (tb < te) {
+    Fetched<D> f[kAhead];
     if (stages) {
-      begin(tb);
-      advance(tb);
+      #pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i].page = page_of(t0 + min(tb + i, te - 1));
+      #pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch_tile(f[i], tb + i);
+      advance(f[0], tb);
     }
-    for (int ti = tb; ti < te; ++ti) {
-      meet();
-      if (stages && ti + 1 < te) advance(ti + 1);
-      if (seen(ti)) {
-        scores(buf[ti & 1]);
-        softmax(buf[ti & 1], (t0 + ti) * kTileTokens);
-        values(buf[ti & 1]);
+    if constexpr (NARROW) {
+      if (stages) {
+        for (int ti = tb; ti < te; ti += 2) {
+          meet();
+          advance(f[1], ti + 1);
+          if (ti + 1 < te) {
+            meet();
+            advance(f[0], ti + 2);
+          }
+        }
+      } else {
+        for (int ti = tb; ti < te; ++ti) {
+          meet();
+          attend(ti);
+        }
+      }
+    } else {
+      for (int ti = tb; ti < te; ++ti) {
+        meet();
+        if (stages) advance(f[0], ti + 1);
+        attend(ti);
       }
     }
   }
   l += __shfl_xor(l, 32, 64);
 
-  // ---- the lane's row: dimensions 32 i + 8 (r / 4) + 4 half + r % 4
-  const bool past = pos >= capacity;  // longer than its page-table row
-  bool last = true;
-  if (splits > 1) {
-    // a run's results: [D + 2][256 rows], so that a wave's lanes store next to each other
-    const int64_t item = x * s.kv_heads + head;
-    const uint32_t bytes = kRowFloats * kTileRows * 4;
-    const auto slot = [&](int sp) {
-      return make_rsrc(slots + (item * splits + sp) * (kRowFloats * kTileRows), bytes);
-    };
-    const uint32_t me = (wave * 32 + n) * 4;
-    if (live) {
-      const rsrc_t rs = slot(split);
-      #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          bstore_dev(rs, (32 * i + 8 * (r >> 2) + 4 * half + (r & 3)) * (kTileRows * 4) + me, 0, o[i][r]);
-      if (half == 0) {
-        bstore_dev(rs, D * (kTileRows * 4) + me, 0, m);
-        bstore_dev(rs, (D + 1) * (kTileRows * 4) + me, 0, l);
-      }
-    }
-    wait_vmem();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int* ctr = counters + kCtrBand + (int)item;
-      const int arrived = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      flag = arrived == splits - 1;
-      if (arrived == splits - 1) store_dev(ctr, 0);
-    }
-    __syncthreads();
-    last = flag != 0;
-    if (last && live) {
-      float big_m = -INFINITY;
-      for (int sp = 0; sp < splits; ++sp) big_m = fmaxf(big_m, bload_dev(slot(sp), D * (kTileRows * 4) + me, 0));
-      l = 0.f;
-      #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        #pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
-      for (int sp = 0; sp < splits; ++sp) {
-        const rsrc_t rs = slot(sp);
-        const float ms = bload_dev(rs, D * (kTileRows * 4) + me, 0);
-        const float k = ms == -INFINITY ? 1.f : fast_exp2(ms - big_m);  // an empty run is zeros
-        l += bload_dev(rs, (D + 1) * (kTileRows * 4) + me, 0) * k;
-        #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            o[i][r] += bload_dev(rs, (32 * i + 8 * (r >> 2) + 4 * half + (r & 3)) * (kTileRows * 4) + me, 0) * k;
-      }
-      m = big_m;
-    }
-  }
   if (any_bad && lane == 0) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
-  if (last && live) {
-    const int64_t at = (int64_t)(q.first + tok) * s.q_heads + qh;
+  // Eight bytes of a row's output and its log-sum; the reciprocal of l.
+  const auto finish = [&](int row, float m, float l, bool first) {
+    const int tok = row / group;
+    const int64_t at = (int64_t)(q.first + tok) * s.q_heads + head * group + row - tok * group;
+    const bool past = start + tok >= capacity;  // longer than its page-table row
     float inv = l == 0.f ? 0.f : 1.f / l;
     if (past) inv = l = __uint_as_float(0x7FC00000u);
+    if (first) {
+      if (a.lse) a.lse[at] = (m + log2f(l)) * kLn2;
+      if (past) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
+    }
+    return std::make_pair(a.out + at * D, inv);
+  };
+  const auto put = [](uint16_t* out, float inv, const float (&v)[4]) {
+    u32x2 w;
+    w.x = pack_bf16(v[0] * inv, v[1] * inv);
+    w.y = pack_bf16(v[2] * inv, v[3] * inv);
+    *reinterpret_cast<u32x2*>(out) = w;
+  };
+
+  // ---- the lane's row: dimensions 32 i + 8 (r / 4) + 4 half + r % 4
+  if (parts == 1) {
+    if (!live) return;
+    const auto [out, inv] = finish(row, m, l, half == 0);
     #pragma unroll
     for (int i = 0; i < D / 32; ++i)
       #pragma unroll
       for (int r = 0; r < 16; r += 4) {
-        u32x2 w;
-        w.x = pack_bf16(o[i][r] * inv, o[i][r + 1] * inv);
-        w.y = pack_bf16(o[i][r + 2] * inv, o[i][r + 3] * inv);
-        *reinterpret_cast<u32x2*>(a.out + at * D + 32 * i + 2 * r + 4 * half) = w;
+        const float v[4] = {o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
+        put(out + 32 * i + 2 * r + 4 * half, inv, v);
       }
+    return;
+  }
+
+  // ---- a run's results: [D / 4][rows][4], then M and l, so that lanes next to
+  // each other store next to each other; the last workgroup joins the runs
+  const int item = x * s.kv_heads + head;
+  const uint32_t bytes = kRowFloats * kTileRows * 4;
+  const auto slot = [&](int sp) {
+    return make_rsrc(slots + (int64_t)(item * splits + sp) * (kRowFloats * kTileRows), bytes);
+  };
+  constexpr uint32_t kAtM = D * kTileRows * 4, kAtL = kAtM + kTileRows * 4;
+  if (live) {
+    const rsrc_t rs = slot(split);
+    const uint32_t me = row - row0;
+    #pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      #pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        bstore16_dev(rs, ((8 * i + (r >> 1) + half) * kTileRows + me) * 16, 0,
+                     f32x4{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]});
     if (half == 0) {
-      if (a.lse) a.lse[at] = (m + log2f(l)) * kLn2;
-      if (past) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
+      bstore_dev(rs, kAtM + me * 4, 0, m);
+      bstore_dev(rs, kAtL + me * 4, 0, l);
     }
   }
+  wait_vmem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int* ctr = counters + kCtrBand + item;
+    const int arrived = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    flag = arrived == parts - 1;
+    if (arrived == parts - 1) store_dev(ctr, 0);
+  }
+  __syncthreads();
+  if (!flag) return;
+  // a thread: kChunk of the D / 4 chunks of a row,
+  // kBatch runs in flight
+  constexpr int kChunk = D / 4 * kTileRows / kThreads, kBatch = NARROW ? 4 : 1;
+  const int r = threadIdx.x % kTileRows, c0 = threadIdx.x / kTileRows * kChunk;
+  if (row0 + r > row1) return;
+  float most = kNever, sum = 0.f;
+  float acc[kChunk][4];
+  #pragma unroll
+  for (int c = 0; c < kChunk; ++c)
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) acc[c][i] = 0.f;
+  for (int p = 0; p < parts; p += kBatch) {
+    float ms[kBatch], ls[kBatch];
+    u32x4 v[kBatch][kChunk];
+    #pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const rsrc_t rs = slot(min(p + i, parts - 1));
+      ms[i] = bload_dev(rs, kAtM + r * 4, 0);
+      ls[i] = bload_dev(rs, kAtL + r * 4, 0);
+      #pragma unroll
+      for (int c = 0; c < kChunk; ++c) v[i][c] = bload16_dev(rs, ((c0 + c) * kTileRows + r) * 16, 0);
+    }
+    float bn = most;
+    #pragma unroll
+    for (int i = 0; i < kBatch; ++i) bn = fmaxf(bn, ms[i]);
+    const float kf = fast_exp2(most - bn);
+    sum *= kf;
+    #pragma unroll
+    for (int c = 0; c < kChunk; ++c)
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) acc[c][j] *= kf;
+    most = bn;
+    #pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (p + i >= parts) break;
+      const float k = fast_exp2(ms[i] - most);
+      sum += ls[i] * k;
+      #pragma unroll
+      for (int c = 0; c < kChunk; ++c)
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) acc[c][j] += __uint_as_float(v[i][c][j]) * k;
+    }
+  }
+  const auto [out, inv] = finish(row0 + r, most, sum, c0 == 0);
+  #pragma unroll
+  for (int c = 0; c < kChunk; ++c) put(out + 4 * (c0 + c), inv, acc[c]);
 }
 
-// A call's rows are taken 256 at a time, or 128 where its sequences have no
-// more on average.
+// A call's rows are taken 128 at a time where its sequences have no more on
+// average, or where that leaves fewer items than half the compute units, so that
+// 256 rows an item would leave long runs or a large join; 256 at a time
+// elsewhere.  Calls of 64 heads of 128 behind 4096 tokens, 128 rows / 256 rows:
+// one chat of 64 tokens 30 / 50 us, of 128 36 / 46, of 256 56 / 57, of 1024
+// 168 / 139; 32 chats of 16 tokens 98 / 123, of 32 197 / 157; 8 chats of 17
+// 55 / 47.
 bool narrow(const KvShape& s, int n_seqs, int tokens) {
-  return (int64_t)tokens * s.group() <= (int64_t)128 * n_seqs;
+  const int64_t rows = ((int64_t)tokens * s.group() + n_seqs - 1) / n_seqs;
+  return rows <= 128 || (rows + 127) / 128 * n_seqs * s.kv_heads < kTileTarget / 2;
 }
 
 // Items of a call are at most this many (their number is device data).
@@ -511,8 +632,8 @@ int64_t item_bound(const KvShape& s, int n_seqs, int tokens, int tile_rows) {
 }  // namespace
 
 size_t kv_prefill_workspace(const KvShape& s) {
-  // items are cut below `target` workgroups, target being as many as fit on
-  // the chip: fewer than 2 target pieces of 256 rows, or of 128 and twice as many
+  // items are cut where there are fewer than the target: into fewer than twice
+  // the target runs, of 256 rows or fewer
   return sizeof(int) * kCounterSlots + sizeof(float) * 2 * kTileTarget * 256 * (s.D + 2);
 }
 
@@ -521,18 +642,20 @@ hipError_t launch_kv_prefill(const KvShape& s, const KvBatch& b, const KvAttenti
   int* counters = static_cast<int*>(workspace);
   float* slots = reinterpret_cast<float*>(counters + kCounterSlots);
   const auto go = [&](auto d, auto z, auto w) {
-    constexpr int D = decltype(d)::value, W = decltype(w)::value;
-    const int64_t target = kTileTarget * (8 / W);
-    const int64_t items = std::max<int64_t>(1, item_bound(s, b.n_seqs, b.tokens, 32 * W));
-    const int splits =
-        (int)std::max<int64_t>(1, std::min<int64_t>(kTileMaxSplits, (target + items - 1) / items));
-    hipLaunchKernelGGL((prefill_attention_kernel<D, decltype(z)::value, W>),
-                       dim3((unsigned)(items * splits)), dim3(64 * W), 0, st, s, b, a, splits, counters,
-                       slots);
+    constexpr int D = decltype(d)::value;
+    constexpr bool N = decltype(w)::value;
+    // the workgroups that the kernel's rule can ask for, whatever the lengths
+    const int64_t items = item_bound(s, b.n_seqs, b.tokens, N ? 128 : 256);
+    const int64_t grid = std::max(items, std::min<int64_t>(items, kTileTarget) + kTileTarget);
+    const auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, s, b, a, counters, slots);
+    };
+    if (b.n_seqs <= 64) launch(prefill_attention_kernel<D, decltype(z)::value, N, true>);
+    else launch(prefill_attention_kernel<D, decltype(z)::value, N, false>);
   };
   const auto pick = [&](auto d, auto z) {
-    if (narrow(s, b.n_seqs, b.tokens)) go(d, z, std::integral_constant<int, 4>{});
-    else go(d, z, std::integral_constant<int, 8>{});
+    if (narrow(s, b.n_seqs, b.tokens)) go(d, z, std::true_type{});
+    else go(d, z, std::false_type{});
   };
   const std::integral_constant<int, 64> d64;
   const std::integral_constant<int, 128> d128;

@@ -95,15 +95,24 @@ KvCache make_kv_cache(const KvShape& s, const uint8_t* codes, const void* scales
                  s.zeros ? const_cast<uint8_t*>(zeros) : nullptr};
 }
 
-// Rows (token, query head of one kv head) a sequence has on average above
-// which a call takes the kernel for many rows.
-constexpr int kDecodeRows = 64;
+// Which calls take the kernel for many rows.  The one for few rows reads and
+// unpacks a cached token again for every 16 rows (token, query head of one kv
+// head) of its sequence, the one for many for every 128 or 256, but it starts
+// and joins slower: it pays from 64 rows a sequence on, or from 128 where 16 at
+// a time make no more items than there are compute units.  Few / many rows'
+// kernel, heads of 128 behind 4096 tokens: 8 chats of 64 rows 29 / 34 us, of 72
+// 37 / 35; 32 chats of 48 77 / 90, of 64 99 / 91; one chat of 128 13.5 / 27; one
+// of 72 behind 65536 59 / 68, of 128 78 / 76, and past that the second wins.
+constexpr int kFewRows = 64, kFewItems = 256;
 
 bool many_rows(const KvShape& s, int n_seqs, int tokens) {
-  return (int64_t)tokens * s.group() > (int64_t)kDecodeRows * n_seqs;
+  const int64_t rows = ((int64_t)tokens * s.group() + n_seqs - 1) / n_seqs;
+  return rows > kFewRows &&
+         (rows > 2 * kFewRows || (rows + 15) / 16 * n_seqs * s.kv_heads > kFewItems);
 }
 
-// Covers every call of at most n_seqs sequences and `tokens` rows.
+// Covers every call of at most `tokens` tokens: one of several sequences that
+// takes the second kernel has more than 128 rows, as one sequence does then too.
 size_t attention_workspace(const KvShape& s, int tokens) {
   const size_t d = kv_decode_workspace(s), p = kv_prefill_workspace(s);
   return many_rows(s, 1, tokens) && p > d ? p : d;
