@@ -75,7 +75,8 @@ typedef struct spear_ec_kv_desc {
  * order; seq_lens[b] counts its tokens including them, so row i of its n is
  * the token at position seq_lens[b] - n + i.  Token j of the sequence lies in
  * page page_table[b][j / page_tokens].  q_offsets must ascend from 0; NULL
- * means one row per sequence (tokens == n_seqs).  Rows behind
+ * means one row per sequence (tokens == n_seqs); with other offsets rows may
+ * be left out or hold anything.  Rows behind
  * q_offsets[n_seqs] belong to no sequence: no call reads or writes them.  A
  * row at a negative position (seq_lens[b] < n) is padding.
  *   n_seqs 0 .. 65536, tokens 0 .. 2^20, tokens * q_heads at most 2^27
@@ -115,8 +116,9 @@ typedef struct spear_ec_kv_rope {
  *   q_out     bf16 rows of q_out_stride elements; may be q itself with the
  *             same stride, and must not overlap any input otherwise.  q and
  *             q_out may both be NULL: nothing but keys and values
- * The rotation is evaluated in 64 bits and quantized without rounding to
- * bf16 in between; quantization is spear_ec_quantize_rtn's over one vector:
+ * What is stored is what 64-bit arithmetic gives, without rounding to bf16
+ * between rotation and quantization; q_out is off by at most (1 + 2^-14) half
+ * steps of bf16.  Quantization is spear_ec_quantize_rtn's over one vector:
  *   symmetric   s = RN_fp16(max|x| / 7), c = clamp(rint(x / s), -8, 7) + 8
  *   asymmetric  lo = min(0, x), hi = max(0, x), s = RN_fp16((hi - lo) / 15),
  *               z = clamp(rint(-lo / s), 0, 15), c = clamp(rint(x / s) + z, 0, 15)

@@ -611,9 +611,9 @@ hipError_t launch_kv_decode(const KvShape& s, const KvBatch& b, const KvAttentio
   int* counters = static_cast<int*>(workspace);
   float* slots = reinterpret_cast<float*>(counters + kCounterSlots);
   const uint32_t bytes = (uint32_t)(kv_decode_workspace(s) - sizeof(int) * kCounterSlots);
-  // at most this many items, of at most this many units: 32-bit sums for the
-  // common calls, one sequence a lane
-  const int64_t items = ((int64_t)b.tokens * s.group() / kRows + b.n_seqs) * s.kv_heads;
+  // at most this many items (also where offsets do not ascend), of at most this
+  // many units: 32-bit sums for the common calls, one sequence a lane
+  const int64_t items = ((int64_t)b.tokens * s.group() / kRows + 1) * b.n_seqs * s.kv_heads;
   const int64_t longest = ((int64_t)s.max_pages << s.page_shift) / kUnit + 2;
   const bool small = b.n_seqs <= 64 && items * longest < (int64_t)1 << 30;
   const auto go = [&](auto kernel) {

@@ -102,8 +102,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
   const int head = blockIdx.x % s.kv_heads;
   const int rest = blockIdx.x / s.kv_heads;
   const auto seq_at = [&](int i) { return load_seq<kTileRows, kTileTokens>(s, b, a.window, i); };
-  const auto cuts = [&](int tiles) {  // runs an item is cut into
-    const int items = tiles * s.kv_heads;
+  const auto cuts = [&](int64_t tiles) {  // runs an item is cut into
+    const int items = (int)min(tiles * s.kv_heads, (int64_t)kTileTarget);
     return items ? min(kTileMaxSplits, (kTileTarget + items - 1) / items) : 1;
   };
   int seq, seq_base, splits;
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
   } else {
     const auto weight = [&](int i) { return (int64_t)seq_at(i).tiles; };
     sum_chunks<kWaves>(before, b.n_seqs, weight);
-    const int tiles = (int)before[(b.n_seqs + 63) / 64];
+    const int64_t tiles = before[(b.n_seqs + 63) / 64];
     splits = cuts(tiles);
     if (rest / splits >= tiles) return;
     int64_t base;
@@ -644,9 +644,10 @@ hipError_t launch_kv_prefill(const KvShape& s, const KvBatch& b, const KvAttenti
   const auto go = [&](auto d, auto z, auto w) {
     constexpr int D = decltype(d)::value;
     constexpr bool N = decltype(w)::value;
-    // the workgroups that the kernel's rule can ask for, whatever the lengths
+    // enough for the kernel's rule whatever the offsets: items are cut below the
+    // target, into fewer than twice the target runs
     const int64_t items = item_bound(s, b.n_seqs, b.tokens, N ? 128 : 256);
-    const int64_t grid = std::max(items, std::min<int64_t>(items, kTileTarget) + kTileTarget);
+    const int64_t grid = std::max<int64_t>(items, 2 * kTileTarget);
     const auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, s, b, a, counters, slots);
     };

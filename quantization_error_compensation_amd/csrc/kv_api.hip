@@ -208,7 +208,8 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
   a.q_stride = q_stride;
   a.cache = make_kv_cache(s, codes, scales, zeros);
   a.scale = softmax_scale;
-  a.window = window;
+  // no row sees more tokens than a page-table row holds
+  a.window = window < s.max_pages << s.page_shift ? window : 0;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   const auto launch = many_rows(s, batch->n_seqs, batch->tokens) ? launch_kv_prefill : launch_kv_decode;

@@ -23,18 +23,6 @@ __device__ __forceinline__ uint32_t f16_01(uint32_t b) {
 __device__ __forceinline__ uint32_t f16_23(uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.f, true));
 }
-// fp16 bytes of 64 + c (0x5400 is 64.0; the four bits under its byte count
-// units).
-__device__ __forceinline__ uint32_t even64(uint32_t w) { return (w << 4) & 0xF0F0F0F0u; }
-__device__ __forceinline__ uint32_t odd64(uint32_t w) { return w & 0xF0F0F0F0u; }
-// Bytes 0, 1 and 2, 3 of b, each under a byte of `top`.
-__device__ __forceinline__ uint32_t pair01(uint32_t b, uint32_t top) {
-  return __builtin_amdgcn_perm(b, top, 0x01050004u);
-}
-__device__ __forceinline__ uint32_t pair23(uint32_t b, uint32_t top) {
-  return __builtin_amdgcn_perm(b, top, 0x01070006u);
-}
-
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ f16x2 as_f16x2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
@@ -202,7 +190,7 @@ __device__ __forceinline__ void sum_chunks(int64_t* before, int n_seqs, F weight
 }
 
 // The sequence that holds work x (which is below the total) and the work
-// before it.  `w` receives the lane's sequence's weight for lanes of the chunk.
+// before it.
 template <typename F>
 __device__ __forceinline__ int find_seq(const int64_t* before, int n_seqs, int64_t x, F weight,
                                         int64_t& seq_base) {

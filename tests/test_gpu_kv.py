@@ -135,6 +135,8 @@ APPENDS = [  # H, G, D, page, asym, lens, new, rope dim, interleaved
     (6, 3, 128, 16, False, [200], [131], 48, True),
     (16, 1, 128, 256, True, [300, 17], [299, 2], 0, False),
     (40, 20, 64, 16, True, [50] * 70, [1 + i % 5 for i in range(70)], 64, False),
+    (8, 2, 64, 16, False, [20 + i for i in range(70)], [9 + i % 12 for i in range(70)], 32, True),
+    (4, 2, 128, 32, True, [80 + i % 40 for i in range(66)], [30] * 66, 128, False),
 ]
 
 
@@ -326,11 +328,149 @@ def test_attention_matches_the_definition(torch, H, G, D, page, asym, lens, new,
     assert torch.equal(out, again) and torch.equal(lse, lse2), "the same call differs"
 
 
-@pytest.mark.parametrize("new", [1, 6, 40])
-def test_attention_empty_and_padded_rows(torch, new):
+SPLITS = [  # the ways a call is cut: H, G, D, page, asym, lens, new, window
+    # one long sequence among short ones: runs that cross items
+    (8, 8, 64, 16, False, [30] * 9 + [4100] + [25] * 15, None, 0),
+    # more than 64 sequences: one token, a few, many rows of 128 and of 256 an item
+    (8, 4, 64, 16, True, [1 + 37 * i % 300 for i in range(70)], None, 0),
+    (4, 2, 128, 16, False, [40 + 11 * i % 200 for i in range(66)], [1 + i % 3 for i in range(66)], 50),
+    (16, 1, 64, 16, False, [20 + 7 * i % 100 for i in range(72)], [6] * 72, 0),
+    (16, 1, 64, 32, True, [9 + 5 * i % 90 for i in range(70)], [9] * 70, 0),
+    # 256 rows an item: whole items, and items cut into runs, one of them short
+    (128, 16, 64, 16, False, [33, 70, 49], [33, 33, 40], 0),
+    (32, 32, 128, 64, True, [700, 150], [130, 130], 0),
+    (32, 32, 64, 64, False, [1100, 131], [131, 131], 600),
+    # 128 rows an item, many runs
+    (8, 1, 128, 16, False, [1500], [17], 0),
+    (8, 1, 64, 64, True, [2500, 4], [40, 4], 1300),
+    # a group of 128 query heads
+    (128, 1, 64, 16, False, [77, 30], [2, 3], 0),
+]
+
+
+@pytest.mark.parametrize("H,G,D,page,asym,lens,new,window", SPLITS)
+def test_attention_however_it_is_cut(torch, H, G, D, page, asym, lens, new, window):
+    note(f"attention cut H={H} G={G} D={D} page={page} asym={asym} {len(lens)} sequences {lens[:3]} "
+         f"new={new and new[:3]} window={window}")
+    c = Case(torch, H, G, D, page, asym, lens, new, seed=H + D + len(lens), offsets=new is not None,
+             extra=2 if new is not None else 0).fill()
+    out, lse, ws = c.attend(window=window)
+    c.check(out, lse, window=window)
+    assert q.spear_ec_workspace_status(ws) == 0
+    again, lse2, _ = c.attend(window=window, ws=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2), "the same call differs"
+
+
+@pytest.mark.parametrize("G,new", [(2, 300), (2, 2)])
+def test_attention_widest_window_with_padding(torch, G, new):
+    """The largest window there is takes in everything, also for rows at negative positions."""
+    note(f"attention widest window new={new}")
+    c = Case(torch, 4, G, 64, 16, True, [200, 150, 1], [new] * 3, seed=12).fill()
+    plain = c.attend()
+    wide = c.attend(window=2 ** 31 - 1)
+    c.check(wide[0], wide[1])
+    assert torch.equal(plain[0], wide[0]) and torch.equal(plain[1], wide[1])
+
+
+@pytest.mark.parametrize("new", [1, 3, 60])
+def test_cache_past_four_gigabytes(torch, new):
+    """Pages whose codes lie 4 GiB and more into the array, written, attended to and read back."""
+    note(f"cache past 4 GiB new={new}")
+    H, G, D, page = 4, 1, 128, 256
+    c = Case(torch, H, G, D, page, False, [300, 70], [new, new], seed=6).fill()
+    pages = (2 ** 32 // (page * D)) + c.pages + 1       # a page's codes: page * D bytes
+    up = pages - c.pages
+    codes = torch.zeros((pages, *c.codes.shape[1:]), dtype=torch.uint8, device="cuda")
+    scales = torch.full((pages, *c.scales.shape[1:]), float("nan"), dtype=torch.float16, device="cuda")
+    assert up * page * D > 2 ** 32
+    codes[up:], scales[up:] = c.codes, c.scales
+    low = c.attend()
+    c.desc = q.make_kv_desc(H, G, D, page, pages, c.max_pages, False)
+    c.d_table.copy_(c.dev(np.where(c.table < 0, c.table, c.table + up)))
+    c.codes, c.scales = codes, scales
+    high = c.attend()
+    c.check(high[0], high[1])
+    assert torch.equal(low[0], high[0]) and torch.equal(low[1], high[1])
+    kv = ref.f64_to_bf16(c.rng.standard_normal((c.rows, G, D)))
+    d = c.bf16(kv)
+    q.spear_ec_kv_append(c.desc, c.batch, None, d, d, None, codes, scales, None, None)
+    ref.append(c.cache, np.zeros((c.rows, H, D), np.uint16), kv, kv, c.offsets, c.lens, c.table)
+    k = torch.full((c.rows, G, D), 7.0, device="cuda")
+    v = torch.full_like(k, 7.0)
+    q.spear_ec_kv_dequant_f32(c.desc, c.batch, codes, scales, None, k, v)
+    torch.cuda.synchronize()
+    assert np.array_equal(codes[up:].cpu().numpy(), c.cache.codes) and not codes[:up].any()
+    for b, m in enumerate(c.lens):
+        for which, x in ((0, k), (1, v)):
+            w, s = c.cache.parts(c.table[b], m, 0, which, m - new)
+            assert np.array_equal(x[c.offsets[b]:c.offsets[b + 1], 0].cpu().numpy(), w * s[:, None])
+
+
+def test_two_captured_calls_share_a_workspace(torch):
+    """A call of few rows and one of many, captured with one workspace and replayed in turn,
+    with eager calls on it in between."""
+    note("captured calls on one workspace")
+    a = Case(torch, 8, 2, 128, 16, True, [2300, 40], [1, 1], seed=21).fill()
+    b = Case(torch, 8, 1, 128, 16, False, [1400], [40], seed=22).fill()
+    both = [(c, c.bf16(c.q)) for c in (a, b)]
+    ra, rb = a.attend(), b.attend()
+    a.check(*ra[:2])
+    b.check(*rb[:2])
+    n = max(q.alloc_kv_workspace(c.desc, len(c.lens), c.rows).numel() for c in (a, b))
+    ws = torch.zeros(n, dtype=ra[2].dtype, device="cuda")
+    outs = [torch.empty_like(r[0]) for r in (ra, rb)]
+    lses = [torch.empty_like(r[1]) for r in (ra, rb)]
+    graphs, st = [], torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i, (c, x) in enumerate(both):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            q.spear_ec_kv_attention(c.desc, c.batch, x, c.codes, c.scales, c.zeros, 128 ** -0.5, outs[i],
+                                    ws, lse=lses[i], stream=st)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for turn in range(4):
+        for i, r in ((0, ra), (1, rb), (0, ra)):
+            outs[i].fill_(float("nan"))
+            lses[i].fill_(float("nan"))
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], r[0]) and torch.equal(lses[i], r[1]), (turn, i)
+            c = both[1 - i][0]
+            eager = c.attend(ws=ws)
+            assert torch.equal(eager[0], (ra, rb)[1 - i][0])
+    assert q.spear_ec_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("new", [2, 70])
+def test_offsets_that_do_not_ascend_stay_in_bounds(torch, new):
+    """Such calls may leave rows out; nothing outside the outputs is touched, and the workspace
+    serves the next call."""
+    note(f"offsets out of order new={new}")
+    c = Case(torch, 8, 2, 64, 16, True, [90, 200, 120], [new] * 3, seed=15, extra=4).fill()
+    good, lse, ws = c.attend()
+    rows = c.bf16(ref.f64_to_bf16(c.rng.standard_normal((c.rows, 2, 64))))
+    for off in ([0, 2 * new, new, 3 * new], [3 * new, 0, 3 * new, 0], [-5, 10 ** 9, -(10 ** 9), 2 ** 31 - 1],
+                [0, 3 * new, 3 * new, 3 * new]):
+        note(f"  {off}")
+        c.d_offsets.copy_(c.dev(np.array(off, np.int32)))
+        c.attend(ws=ws)
+        back = torch.zeros((c.rows, 2, 64), device="cuda")
+        q.spear_ec_kv_dequant_f32(c.desc, c.batch, c.codes, c.scales, c.zeros, back, back.clone())
+        q.spear_ec_kv_append(c.desc, c.batch, None, rows, rows, None, c.codes.clone(), c.scales.clone(),
+                             c.zeros.clone(), None)
+        torch.cuda.synchronize()
+        q.spear_ec_workspace_status(ws)
+        c.d_offsets.copy_(c.dev(c.offsets.astype(np.int32)))
+        again, lse2, _ = c.attend(ws=ws)
+        assert torch.equal(good, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("new,H,G", [(1, 8, 2), (6, 8, 2), (40, 8, 2), (40, 256, 32)])
+def test_attention_empty_and_padded_rows(torch, new, H, G):
     """Sequences of length 0, padding rows, no rows, and rows behind the last sequence."""
-    note(f"attention empty rows new={new}")
-    c = Case(torch, 8, 2, 64, 16, True, [0, 3, 60, 0, 20], [new, new, new, 0, 1], seed=new, extra=5).fill()
+    note(f"attention empty rows new={new} H={H} G={G}")
+    c = Case(torch, H, G, 64, 16, True, [0, 3, 60, 0, 20], [new, new, new, 0, 1], seed=new, extra=5).fill()
     out, lse, ws = c.attend()
     c.check(out, lse)
     o = out.float()
@@ -338,7 +478,7 @@ def test_attention_empty_and_padded_rows(torch, new):
     assert q.spear_ec_workspace_status(ws) == 0
 
 
-@pytest.mark.parametrize("H,G,D,new", [(8, 2, 128, 1), (4, 1, 64, 20), (16, 2, 128, 9)])
+@pytest.mark.parametrize("H,G,D,new", [(8, 2, 128, 1), (4, 1, 64, 20), (16, 2, 128, 9), (64, 16, 64, 50)])
 def test_attention_peaks_and_value_scales(torch, H, G, D, new):
     """Scores from flat to a single peak, a first token with tiny values that takes most of the
     weight, scales over many powers of two, and softmax scales far from 1 / sqrt(D)."""
@@ -382,12 +522,12 @@ def test_attention_query_extremes_stay_in_their_row(torch):
     assert (np.abs(o - ro) <= tol)[mask].all()
 
 
-@pytest.mark.parametrize("new", [1, 9, 50])
-def test_attention_bad_pages_give_nan_and_the_error_bit(torch, new):
+@pytest.mark.parametrize("new,H,G", [(1, 8, 2), (9, 8, 2), (50, 8, 2), (50, 64, 16)])
+def test_attention_bad_pages_give_nan_and_the_error_bit(torch, new, H, G):
     """Page numbers outside the cache and sequences longer than their page-table row: NaN in the
     rows that attend to them, the workspace's error bit, and nothing else touched."""
-    note(f"attention bad pages new={new}")
-    c = Case(torch, 8, 2, 128, 16, True, [200, 90, 100, 70], [new] * 4, seed=new).fill()
+    note(f"attention bad pages new={new} H={H} G={G}")
+    c = Case(torch, H, G, 128, 16, True, [200, 90, 100, 70], [new] * 4, seed=new).fill()
     good = c.table.copy()
     bad = good.copy()
     bad[0, 3] = c.pages
