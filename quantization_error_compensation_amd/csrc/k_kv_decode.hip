@@ -179,7 +179,10 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
   if (items == 0) return;
   const count_t run = max((count_t)((units + kGroups - 1) / kGroups), (count_t)kWaves);
   // k pieces an item: as many as there are workgroups for, then as few as
-  // take no more steps of the four waves
+  // take no more steps of the waves.  Pieces / runs: one chat of 1000 tokens with
+  // 32 heads 7.7 / 23.9 us (runs are a step of all waves at least), 16 chats up to
+  // 4096 16.5 / 19.6, 30 chats of 4096 28 / 32, but 20 of 8192, whose 160 items
+  // leave a third of the workgroups without one, 48 / 42.
   int k = 0;
   if (items <= kGroups) {
     k = kGroups / (int)items;
@@ -324,6 +327,9 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
       const int j0 = (q.u0 + pc.ub + ui) * kUnit;
       const bool more = ui + kWaves < pc.take;
       load_values(u, a.cache, vblk, n);
+      // all of them before the scores: scheduled among the matrix steps they were
+      // issued later and took registers the longer (131001 tokens: 40.5 us; so 37.5)
+      __builtin_amdgcn_sched_barrier(0);
       float x[32];
       const float init = (ZEROS ? 0.f : -8.f) * qs;
       #pragma unroll
