@@ -79,6 +79,8 @@ def make_kv_batch(q_offsets, seq_lens, page_table, tokens: int) -> spear_ec_kv_b
             continue
         if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
             raise ValueError(f"a batch array must be contiguous int32 of shape {shape}")
+    if any(t is not None and t.get_device() != seq_lens.get_device() for t, _ in shapes):
+        raise ValueError("the batch arrays must be on one device")
     b = spear_ec_kv_batch(n, int(tokens), None if q_offsets is None else q_offsets.data_ptr(),
                           seq_lens.data_ptr(), page_table.data_ptr())
     b.arrays = (q_offsets, seq_lens, page_table)
@@ -116,49 +118,60 @@ def spear_ec_kv_workspace_bytes(desc, n_seqs: int, tokens: int) -> int:
     return int(_lib().spear_ec_kv_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(tokens)))
 
 
-def _current_stream(stream, t):
-    """Raw handle of the stream, by default the current one of t's device."""
+def _call(fn, device, stream, *args):
+    """fn on the device, on the stream (by default the device's current one)."""
+    import torch
+    if device < 0:
+        raise ValueError("the tensors must be on the GPU")
     if stream is None:
-        import torch
-        if t.device.type != "cuda":
-            raise ValueError("the tensors must be on the GPU")
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
-def _rows(t, tokens, heads, dim, dtype, name, strided=True):
-    """Row stride of a token array, checked against what the call will read or write."""
+def _rows(t, device, tokens, heads, dim, dtype, name, strided=True):
+    """Pointer and row stride of a token array, checked against what the call
+    will read or write."""
     shape = t.shape
     if t.dtype is not dtype or len(shape) != 3 or shape[0] < tokens or shape[1] != heads or \
-            shape[2] != dim:
-        raise ValueError(f"{name} must be {dtype} of shape [>= {tokens}, {heads}, {dim}]")
+            shape[2] != dim or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} of shape [>= {tokens}, {heads}, {dim}] on the "
+                         "cache's device")
     row, head, one = t.stride()
     if shape[0] <= 1:
         row = heads * dim
     if one != 1 or (head != dim and heads > 1) or (not strided and row != heads * dim):
         raise ValueError(f"{name}'s rows must be contiguous [{heads}, {dim}]")
-    return row
+    return t.data_ptr(), row
 
 
-def _cache(desc, codes, scales, zeros):
-    """Pointers of the cache arrays, checked against the desc."""
-    blocks, D = desc.page_tokens // 16, desc.head_dim
-    pages, heads = desc.pages, desc.kv_heads
-    ok = codes.shape == (pages, heads, blocks, 16 * D) and codes.element_size() == 1 and \
-        codes.is_contiguous() and scales.shape == (pages, heads, blocks, 2, 16) and \
-        scales.element_size() == 2 and scales.is_contiguous()
+def _flat(t, device, elements, size):
+    return t.numel() == elements and t.element_size() == size and t.is_contiguous() and \
+        t.get_device() == device
+
+
+def _cache(desc, batch, codes, scales, zeros):
+    """Device and pointers of the cache arrays, checked against the desc, as is
+    the batch."""
+    device = codes.get_device()
+    tokens = desc.pages * desc.kv_heads * desc.page_tokens
+    ok = _flat(codes, device, tokens * desc.head_dim, 1) and _flat(scales, device, tokens * 2, 2)
     if desc.flags & SPEAR_EC_ZEROS:
-        ok = ok and zeros is not None and zeros.shape == (pages, heads, blocks, 16) and \
-            zeros.element_size() == 1 and zeros.is_contiguous()
+        ok = ok and zeros is not None and _flat(zeros, device, tokens, 1)
     if not ok:
-        raise ValueError("codes, scales and zeros must have the shapes of kv_cache_shapes(desc)")
-    return codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr()
-
-
-def _table(desc, batch):
+        raise ValueError("codes, scales and zeros must have the shapes of kv_cache_shapes(desc), "
+                         "on one device")
     arrays = getattr(batch, "arrays", None)
-    if arrays and arrays[2].shape[1] != desc.max_pages:
-        raise ValueError("page_table's rows must have desc.max_pages entries")
+    if arrays and (arrays[2].shape[1] != desc.max_pages or arrays[2].get_device() != device):
+        raise ValueError("page_table's rows must have desc.max_pages entries, on the cache's device")
+    return device, codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr()
 
 
 def spear_ec_kv_append(desc, batch, q, k, v, cos_sin, codes, scales, zeros, q_out,
@@ -166,27 +179,21 @@ def spear_ec_kv_append(desc, batch, q, k, v, cos_sin, codes, scales, zeros, q_ou
     """Rotate q (to q_out) and k by cos_sin (fp32 [rows, dim], or None) and
     store k and v in the cache; q and q_out may be None."""
     import torch
-    n, D, bf16 = batch.tokens, desc.head_dim, torch.bfloat16
-    _table(desc, batch)
-    cache = _cache(desc, codes, scales, zeros)
-    ks = _rows(k, n, desc.kv_heads, D, bf16, "k")
-    vs = _rows(v, n, desc.kv_heads, D, bf16, "v")
-    qp = op = None
-    qs = os = 0
-    if q is not None:
-        qs, qp = _rows(q, n, desc.q_heads, D, bf16, "q"), q.data_ptr()
-    if q_out is not None:
-        os, op = _rows(q_out, n, desc.q_heads, D, bf16, "q_out"), q_out.data_ptr()
+    n, D, H, G, bf16 = batch.tokens, desc.head_dim, desc.q_heads, desc.kv_heads, torch.bfloat16
+    dev, cp, sp, zp = _cache(desc, batch, codes, scales, zeros)
+    kp, ks = _rows(k, dev, n, G, D, bf16, "k")
+    vp, vs = _rows(v, dev, n, G, D, bf16, "v")
+    qp, qs = _rows(q, dev, n, H, D, bf16, "q") if q is not None else (None, 0)
+    op, os = _rows(q_out, dev, n, H, D, bf16, "q_out") if q_out is not None else (None, 0)
     rope = None
     if cos_sin is not None:
         shape = cos_sin.shape
-        if cos_sin.dtype is not torch.float32 or len(shape) != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous fp32 [rows, dim]")
+        if cos_sin.dtype is not torch.float32 or len(shape) != 2 or not cos_sin.is_contiguous() or \
+                cos_sin.get_device() != dev:
+            raise ValueError("cos_sin must be a contiguous fp32 [rows, dim] on the cache's device")
         rope = spear_ec_kv_rope(cos_sin.data_ptr(), shape[0], shape[1], interleaved)
-    status = _lib().spear_ec_kv_append(desc, batch, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, rope,
-                                       *cache, op, os, _current_stream(stream, codes))
-    if status:
-        _check(status)
+    _call(_lib().spear_ec_kv_append, dev, stream, desc, batch, qp, qs, kp, ks, vp, vs, rope, cp, sp, zp,
+          op, os)
 
 
 def spear_ec_kv_attention(desc, batch, q, codes, scales, zeros, softmax_scale, out, workspace,
@@ -195,34 +202,30 @@ def spear_ec_kv_attention(desc, batch, q, codes, scales, zeros, softmax_scale, o
     lse, fp32 [tokens, q_heads])."""
     import torch
     n, H, D = batch.tokens, desc.q_heads, desc.head_dim
-    _table(desc, batch)
-    cache = _cache(desc, codes, scales, zeros)
-    qs = _rows(q, n, H, D, torch.bfloat16, "q")
-    _rows(out, n, H, D, torch.bfloat16, "out", strided=False)
+    dev, cp, sp, zp = _cache(desc, batch, codes, scales, zeros)
+    qp, qs = _rows(q, dev, n, H, D, torch.bfloat16, "q")
+    op, _ = _rows(out, dev, n, H, D, torch.bfloat16, "out", strided=False)
     lp = None
     if lse is not None:
         shape = lse.shape
         if lse.dtype is not torch.float32 or len(shape) != 2 or shape[0] < n or shape[1] != H or \
-                not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous fp32 of shape [>= {n}, {H}]")
+                not lse.is_contiguous() or lse.get_device() != dev:
+            raise ValueError(f"lse must be contiguous fp32 of shape [>= {n}, {H}] on the cache's device")
         lp = lse.data_ptr()
-    wp, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
-    status = _lib().spear_ec_kv_attention(desc, batch, q.data_ptr(), qs, *cache, softmax_scale, window,
-                                          out.data_ptr(), lp, wp, ws_bytes,
-                                          _current_stream(stream, codes))
-    if status:
-        _check(status)
+    wp, size = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous, on the cache's device")
+        wp, size = workspace.data_ptr(), workspace.nbytes
+    _call(_lib().spear_ec_kv_attention, dev, stream, desc, batch, qp, qs, cp, sp, zp, softmax_scale,
+          window, op, lp, wp, size)
 
 
 def spear_ec_kv_dequant_f32(desc, batch, codes, scales, zeros, k_out, v_out, stream=None):
     """The batch's rows of the cache as fp32 values [tokens, kv_heads, head_dim]."""
     import torch
     n, G, D = batch.tokens, desc.kv_heads, desc.head_dim
-    _table(desc, batch)
-    cache = _cache(desc, codes, scales, zeros)
-    _rows(k_out, n, G, D, torch.float32, "k_out", strided=False)
-    _rows(v_out, n, G, D, torch.float32, "v_out", strided=False)
-    status = _lib().spear_ec_kv_dequant_f32(desc, batch, *cache, k_out.data_ptr(), v_out.data_ptr(),
-                                            _current_stream(stream, codes))
-    if status:
-        _check(status)
+    dev, cp, sp, zp = _cache(desc, batch, codes, scales, zeros)
+    kp, _ = _rows(k_out, dev, n, G, D, torch.float32, "k_out", strided=False)
+    vp, _ = _rows(v_out, dev, n, G, D, torch.float32, "v_out", strided=False)
+    _call(_lib().spear_ec_kv_dequant_f32, dev, stream, desc, batch, cp, sp, zp, kp, vp)

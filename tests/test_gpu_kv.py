@@ -563,6 +563,36 @@ def test_attention_strided_queries_and_no_lse(torch):
     c.check(out, None)
 
 
+def test_tensors_of_the_host_are_refused(torch):
+    note("tensors of the host")
+    c = Case(torch, 4, 2, 64, 16, True, [20, 7], [1, 1], seed=1).fill()
+    x, out = c.bf16(c.q), torch.empty((2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    kv = x[:, :2].contiguous()
+    ws = q.alloc_kv_workspace(c.desc, 2, 2)
+    cs = torch.zeros((30, 64), device="cuda")
+    cache = (c.codes, c.scales, c.zeros)
+
+    def attend(x=x, cache=cache, out=out, ws=ws, lse=None):
+        q.spear_ec_kv_attention(c.desc, c.batch, x, *cache, 0.1, out, ws, lse=lse)
+
+    def append(x=x, k=kv, cs=cs, out=out):
+        q.spear_ec_kv_append(c.desc, c.batch, x, k, kv, cs, *cache, out)
+
+    attend()
+    append()
+    for f, kw in ((attend, dict(x=x.cpu())), (attend, dict(out=out.cpu())), (attend, dict(ws=ws.cpu())),
+                  (attend, dict(lse=torch.zeros(2, 4))), (attend, dict(cache=(c.codes, c.scales.cpu(), c.zeros))),
+                  (attend, dict(cache=tuple(t.cpu() for t in cache))), (append, dict(x=x.cpu())),
+                  (append, dict(k=kv.cpu())), (append, dict(cs=cs.cpu())), (append, dict(out=out.cpu()))):
+        with pytest.raises(ValueError):
+            f(**kw)
+    with pytest.raises(ValueError):
+        q.spear_ec_kv_dequant_f32(c.desc, c.batch, *cache, kv.float(), kv.float().cpu())
+    with pytest.raises(ValueError):
+        q.make_kv_batch(c.d_offsets, c.d_lens.cpu(), c.d_table, 2)
+    torch.cuda.synchronize()
+
+
 def test_attention_on_two_streams_at_once(torch):
     note("attention on two streams")
     a = Case(torch, 8, 2, 128, 16, True, [900, 333], [1, 1], seed=1).fill()

@@ -186,6 +186,34 @@ def test_binding_refuses_tensors_the_call_would_misread(lib):
         q.spear_ec_kv_attention(d, wide, good["q"], codes, scales, zeros, 0.1, good["o"], None)
 
 
+    with pytest.raises(ValueError, match="on the GPU"):
+        q.spear_ec_kv_attention(d, b, good["q"], codes, scales, zeros, 0.1, good["o"], None)
+
+
+def test_binding_runs_on_the_cache_s_device(monkeypatch):
+    """A call for tensors of another device than the current one runs with theirs current, on
+    its stream."""
+    import contextlib
+    import torch
+    seen = []
+
+    @contextlib.contextmanager
+    def device(i):
+        seen.append(("enter", i))
+        yield
+        seen.append(("leave", i))
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    fn = lambda *a: seen.append(a) or 0  # noqa: E731
+    kv._call(fn, 1, None, "x")
+    kv._call(fn, 0, None, "y")
+    kv._call(fn, 1, 7, "z")
+    assert seen == [("enter", 1), ("x", 101), ("leave", 1), ("y", 100), ("enter", 1), ("z", 7),
+                    ("leave", 1)]
+
+
 # ------------------------------------------------------------- the reference
 def test_reference_quantizer_by_hand():
     c, s, z = ref.quantize(np.array([7.0, -7.0, 3.5, 0.0]), False)
