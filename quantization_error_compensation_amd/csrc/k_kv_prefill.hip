@@ -36,12 +36,13 @@
 // 4096 and a chunk of 512 tokens, so: 789 and 159 us).
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
-// steps and takes about 4600: some 3000 of vector work (two thirds of it the
-// softmax, the rest unpacking) and 2300 of LDS reads run beside them, and two
-// waves a SIMD, all that 230 registers leave room for, do not overlap them
-// further.  Computing a tile's scores beside the previous tile's softmax in
-// one wave, with eight or four waves a workgroup, took 1.09 to 1.2 times as
-// long; wave priorities changed nothing.
+// steps and takes about 4500 (prompts of 4096 tokens 764-783 us, 890 TFLOP/s).
+// Counters there: matrix cores busy 38% of the time, vector units 50%, LDS 34%:
+// two waves a SIMD, all that 230 registers leave room for, wait for each other's
+// results rather than for one unit (32 fewer vector instructions a tile in the
+// staging waves gained 0.5%).  Computing a tile's scores beside the previous
+// tile's softmax in one wave, with eight or four waves a workgroup, took 1.09 to
+// 1.2 times as long; staging by all waves and wave priorities gained nothing.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -303,11 +304,15 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
       if (lane == 0) to.e[part] = (float)e;
       #pragma unroll
       for (int i = 0; i < D / 64; ++i) {  // 8 tokens: one chunk of two dimensions
-        f16x2 z[4], sg[4];
+        f16x2 z[4], sg[4];  // less the zero-point: before the scale, or with it for 8
+        const auto value = [](uint32_t c, f16x2 z, f16x2 sg) {
+          if constexpr (ZEROS) return as_u32((as_f16x2(c) + z) * sg);
+          else return as_u32(__builtin_elementwise_fma(as_f16x2(c), sg, z));
+        };
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
           sg[j] = as_f16x2(vs[4 * i + j]) * as_f16x2(unit);
-          z[j] = as_f16x2(0xC800C800u);
+          z[j] = sg[j] * as_f16x2(0xC800C800u);  // -8 of them, exact
         }
         if constexpr (ZEROS) {
           const uint32_t a0 = high_codes(fe.vz[2 * i]) | 0x80808080u;
@@ -321,10 +326,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
         for (int odd = 0; odd < 2; ++odd) {
           const uint32_t w0 = odd ? high_codes(fe.v[2 * i]) : low_codes(fe.v[2 * i]);
           const uint32_t w1 = odd ? high_codes(fe.v[2 * i + 1]) : low_codes(fe.v[2 * i + 1]);
-          const u32x4 c = {as_u32((as_f16x2(f16_01(w0)) + z[0]) * sg[0]),
-                           as_u32((as_f16x2(f16_23(w0)) + z[1]) * sg[1]),
-                           as_u32((as_f16x2(f16_01(w1)) + z[2]) * sg[2]),
-                           as_u32((as_f16x2(f16_23(w1)) + z[3]) * sg[3])};
+          const u32x4 c = {value(f16_01(w0), z[0], sg[0]), value(f16_23(w0), z[1], sg[1]),
+                           value(f16_01(w1), z[2], sg[2]), value(f16_23(w1), z[3], sg[3])};
           *reinterpret_cast<u32x4*>(&to.v[2 * col + odd][16 * part + 8 * (i + half_col)]) = c;
         }
       }
@@ -344,6 +347,17 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     const int j0 = (t0 + ti) * kTileTokens;
     return j0 <= any_hi && j0 + kTileTokens - 1 >= any_lo;
   };
+  // Order of D / 8 matrix steps and the reads of their operands: four ahead (none
+  // set: prompts of 4096 tokens 793 us, for the scores 780, for both 773).
+  const auto read_ahead = [] {
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+    #pragma unroll
+    for (int i = 0; i < D / 8 - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+  };
   const auto scores = [&](const Staged<D>& st) {
     #pragma unroll
     for (int r = 0; r < 16; ++r) sc[0][r] = sc[1][r] = 0.f;
@@ -354,14 +368,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
         const u32x4 kf = *reinterpret_cast<const u32x4*>(&st.k[32 * t + n][16 * i + 8 * half]);
         sc[t] = mfma32x32x16_f16(kf, qf[i], sc[t]);
       }
-    // reads four operands ahead of the matrix steps
-    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-    #pragma unroll
-    for (int i = 0; i < D / 8 - 4; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+    read_ahead();
   };
   // The lane's tokens of a tile: 16 g + 8 half + 0 .. 7 for g = 0 .. 3.
   const auto key_scale = [&](const Staged<D>& st, int g, f32x4 (&k)[2]) {
@@ -440,6 +447,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
         const u32x4 vf = *reinterpret_cast<const u32x4*>(&st.v[32 * i + n][16 * g + 8 * half]);
         o[i] = mfma32x32x16_f16(vf, pf[g], o[i]);
       }
+    read_ahead();
   };
   // What the waves hand each other lies in LDS: nothing else is waited for.
   const auto meet = [&] {
