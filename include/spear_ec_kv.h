@@ -155,7 +155,7 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  * Keys meet q exactly and products and sums are held in fp32; a probability
  * and a value are rounded to fp16 on their way (2^-11 relative each).
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
- * finite and positive.  A q row holding an infinity or NaN gives NaN in that
+ * positive and at most 2^64.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.
  */
 int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch* batch,

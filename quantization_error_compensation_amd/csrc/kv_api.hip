@@ -187,8 +187,8 @@ int spear_ec_kv_attention(const spear_ec_kv_desc* desc, const spear_ec_kv_batch*
   int rc = check_kv_desc(desc);
   if (!rc) rc = check_kv_batch(desc, batch);
   if (rc) return rc;
-  if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f)
-    return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "softmax_scale must be finite and positive");
+  if (!(softmax_scale > 0.f) || softmax_scale > 0x1p64f)  // past that scores leave fp32
+    return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "softmax_scale must be positive and at most 2^64");
   if (window < 0) return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "window is negative");
   if (batch->n_seqs == 0 || batch->tokens == 0) return SPEAR_EC_OK;
   rc = check_kv_cache(desc, codes, scales, zeros);

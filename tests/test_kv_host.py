@@ -134,7 +134,7 @@ def test_attention_and_dequant_refusals(lib):
     for change, code in (
             (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(out=ptr(0)), INVALID),
             (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
-            (dict(scale=float("inf")), INVALID), (dict(window=-1), INVALID),
+            (dict(scale=float("inf")), INVALID), (dict(scale=2.0 ** 65), INVALID), (dict(window=-1), INVALID),
             (dict(qs=1023), INVALID), (dict(qs=1028), MISALIGNED), (dict(q=ptr(0) + 4), MISALIGNED),
             (dict(out=ptr(6) + 2), MISALIGNED), (dict(lse=ptr(12) + 2), MISALIGNED),
             (dict(ws=None), WORKSPACE), (dict(ws=ptr(7) + 8), MISALIGNED), (dict(ws_bytes=64), WORKSPACE)):
