@@ -13,8 +13,9 @@
 // (c - z) s 2^-e with e the exponent of the block's largest scale, rounded
 // once (2^-11).  Two waves share a SIMD, w and w + 4; the first stages the next
 // tile before its own work on this one, so that its matrix steps meet the
-// other's vector work (staging by all eight after their work: 868 us for
-// prompts of 4096 tokens with 64 heads of 128, so: 802 us).  Items of 128 rows
+// other's vector work (staging by all eight waves, half a block each, before
+// their work: 817 us for prompts of 4096 tokens with 64 heads of 128, by waves
+// 4-7 after theirs: 812, so: 785 on the same card).  Items of 128 rows
 // leave the staging to waves 0-3 alone, two tiles ahead, and the rows to waves
 // 4-7: such calls read the cache more often per row, and waited for it (8 chats
 // of 72 rows behind 4096 tokens: two workgroups of four waves a compute unit

@@ -100,9 +100,9 @@ KvCache make_kv_cache(const KvShape& s, const uint8_t* codes, const void* scales
 // head) of its sequence, the one for many for every 128 or 256, but it starts
 // and joins slower: it pays from 64 rows a sequence on, or from 128 where 16 at
 // a time make no more items than there are compute units.  Few / many rows'
-// kernel, heads of 128 behind 4096 tokens: 8 chats of 64 rows 29 / 34 us, of 72
-// 37 / 35; 32 chats of 48 77 / 90, of 64 99 / 91; one chat of 128 13.5 / 27; one
-// of 72 behind 65536 59 / 68, of 128 78 / 76, and past that the second wins.
+// kernel, heads of 128 behind 4096 tokens: 8 chats of 64 rows 25 / 33 us, of 72
+// 37 / 35, of 128 47 / 38; 32 chats of 48 78 / 89, of 64 101 / 89; one chat of
+// 128 13 / 27; one of 72 behind 65536 57 / 68, of 128 78 / 75, of 192 118 / 103.
 constexpr int kFewRows = 64, kFewItems = 256;
 
 bool many_rows(const KvShape& s, int n_seqs, int tokens) {
