@@ -5,12 +5,12 @@
 // Work.  The rows (token, query head) of a sequence that read one kv head are
 // taken 16 at a time; an item is one such row tile and one kv head, a unit 128
 // tokens of an item.  The lengths are device data, so every workgroup adds them
-// up itself.  Either each item is cut into the same number of pieces, one a
-// workgroup, the row tiles of one piece next to each other on one XCD, whose L2
-// then reads the cache once for them (8 chats of 64 rows behind 4096 tokens 29
-// -> 25 us); or, where uneven lengths would make the longest piece more than a
-// step longer than an even share, the workgroups take equal runs of all items'
-// units laid end to end.  The waves of a workgroup take every eighth unit.
+// up itself.  Either the items are cut into pieces of one size, one a workgroup,
+// the row tiles of one piece next to each other on one XCD, whose L2 then reads
+// the cache once for them (8 chats of 64 rows behind 4096 tokens 29 -> 25 us);
+// or, where that would make the longest piece more than a step longer than an
+// even share, the workgroups take equal runs of all items' units laid end to
+// end.  The waves of a workgroup take every eighth unit.
 // Each workgroup that holds a piece of a cut item leaves (O, M, l) in its slot
 // of the workspace, and the last one to arrive joins them in order, so results
 // do not depend on the order of arrival.
@@ -134,7 +134,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) { return (int6
 struct Piece {
   int seq, head, tile;
   int ub, take;           // its units of the item
-  int parts, part;        // pieces the item is cut into, this one's number
+  int parts, part;        // pieces of the item, this one's number
   int counter;            // arrival counter of the item (its first workgroup)
   int slot0, slot1, step; // slots of piece 0 and 1; the others follow by step
 };
@@ -147,6 +147,11 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
   __shared__ float osh[kWaves][kRows][D + 4];
   __shared__ float msh[kRows][kRows], lsh[kRows][kRows];
   __shared__ int flag;
+  // what the loop over units does not use, out of the registers: the lanes'
+  // sequences and work up to them (SMALL), the piece
+  __shared__ Seq seqs[SMALL ? 64 : 1];
+  __shared__ int uptos[SMALL ? 64 : 1];
+  __shared__ Piece kept;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int n = lane & 15, kb = lane >> 4;
   const int capacity = s.max_pages << s.page_shift;
@@ -158,14 +163,13 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
   count_t units = 0, items = 0;
   int longest = 0;
   Seq own{0, 0, 0, 0, 0, 1};  // SMALL: the lane's sequence
-  count_t upto_items = 0, upto_units = 0;
+  count_t upto = 0;
   if constexpr (SMALL) {
     if (lane < b.n_seqs) own = seq_at(lane);
     const int it = own.tiles * s.kv_heads;
-    upto_items = wave_prefix(it);
-    upto_units = wave_prefix(it * own.nb);
-    items = __builtin_amdgcn_readlane(upto_items, 63);
-    units = __builtin_amdgcn_readlane(upto_units, 63);
+        upto = wave_prefix(it * own.nb);
+    items = __builtin_amdgcn_readlane(wave_prefix(it), 63);
+    units = __builtin_amdgcn_readlane(upto, 63);
     longest = wave_max(it ? own.nb : 0);
   } else {
     for (int i = lane; i < b.n_seqs; i += 64) {
@@ -181,27 +185,65 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
   }
   if (items == 0) return;
   const count_t run = max((count_t)((units + kGroups - 1) / kGroups), (count_t)kWaves);
-  // k pieces an item: as many as there are workgroups for, then as few as
-  // take no more steps of the waves.  Pieces / runs: one chat of 1000 tokens with
-  // 32 heads 7.7 / 23.9 us (runs are a step of all waves at least), 16 chats up to
-  // 4096 16.5 / 19.6, 30 chats of 4096 28 / 32, but 20 of 8192, whose 160 items
-  // leave a third of the workgroups without one, 48 / 42.
-  int k = 0;
+  // Pieces of at most c units, one a workgroup and no more of them than there
+  // are: as many for each item as for the longest, or, an item's last piece being
+  // short, units / c + items of them, or, uneven lengths filling fewer, what lies
+  // between that and an even share; at least a step of the waves.  Pieces / runs:
+  // one chat of 1000 tokens with 32 heads 7.7 / 23.9 us (runs are a step of all
+  // waves at least), 16 chats up to 4096 16.5 / 19.6, 30 chats of 4096 28 / 32,
+  // but 20 of 8192, whose 160 items leave a third of the workgroups without one,
+  // 48 / 42.  With as many pieces for each item as for the longest alone: 12
+  // chats up to 4096 tokens 20.0 us, so 17.5; one to 16 even ones 0.1 to 0.3 less.
+  int c = 0;
   if (items <= kGroups) {
-    k = kGroups / (int)items;
-    const int even = (int)((run + kWaves - 1) / kWaves);
-    const int steps = ((longest + k - 1) / k + kWaves - 1) / kWaves;
-    if (steps <= even + 1) k = (longest + kWaves * steps - 1) / (kWaves * steps);
-    else
-      k = 0;
+    const auto steps = [](int c) { return (c + kWaves - 1) / kWaves; };
+    const int even = (int)((units + kGroups - 1) / kGroups);
+    const int k = kGroups / (int)items;
+    c = (longest + k - 1) / k;
+    if (c > kWaves) {
+      const int spare = kGroups - (int)items;
+      if (spare) c = (int)min((count_t)c, (count_t)((units + spare - 1) / spare));
+      if constexpr (SMALL) {
+        int low = max(even, kWaves);
+        while (low < c && (c - low > low / 16 || steps(low) < steps(c))) {
+          const int mid = (low + c) / 2;
+          const int n = own.tiles * s.kv_heads * ((own.nb + mid - 1) / mid);
+          if (__builtin_amdgcn_readlane(wave_prefix(n), 63) <= kGroups) c = mid;
+          else low = mid + 1;
+        }
+      }
+    }
+    c = max(c, kWaves);
+    if (steps(c) > steps(even) + 1) c = 0;
+  }
+  count_t pieces = 0;
+  const auto parts_of = [&](const Seq& q) { return (q.nb + c - 1) / c; };
+  if constexpr (SMALL)
+    if (c) {
+      upto = wave_prefix(own.tiles * s.kv_heads * parts_of(own));
+      pieces = __builtin_amdgcn_readlane(upto, 63);
+    }
+  if constexpr (SMALL) {  // every wave the same
+    seqs[lane] = own;
+    uptos[lane] = upto;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   const int me = (int)(blockIdx.x % kXcds) * (kGroups / kXcds) + (int)(blockIdx.x / kXcds);
-  count_t x0 = k ? (count_t)me : (count_t)me * run;
-  const count_t x1 = k ? min(x0 + 1, items * k) : min(x0 + run, units);
+  if constexpr (!SMALL)
+    if (c) {
+      int64_t n = 0;
+      for (int i = lane; i < b.n_seqs; i += 64) {
+        const Seq q = seq_at(i);
+        n += (int64_t)q.tiles * s.kv_heads * parts_of(q);
+      }
+      pieces = wave_sum(n);
+    }
+  count_t x0 = c ? (count_t)me : (count_t)me * run;
+  const count_t x1 = c ? min(x0 + 1, pieces) : min(x0 + run, units);
   if (x0 >= x1) return;
   const auto weight = [&](int i) {
     const Seq q = seq_at(i);
-    return (int64_t)q.tiles * s.kv_heads * (k ? k : q.nb);
+    return (int64_t)q.tiles * s.kv_heads * (c ? parts_of(q) : q.nb);
   };
   if constexpr (!SMALL)
     if (b.n_seqs > 64) sum_chunks<kWaves>(before, b.n_seqs, weight);
@@ -212,16 +254,16 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
     Piece pc;
     count_t seq_base;
     if constexpr (SMALL) {
-      const count_t upto = k ? upto_items * k : upto_units;
-      const int who = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(upto > x0)) - 1);
+      const int who = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(uptos[lane] > x0)) - 1);
       pc.seq = who;
-      q.first = __builtin_amdgcn_readlane(own.first, who);
-      q.n = __builtin_amdgcn_readlane(own.n, who);
-      q.len = __builtin_amdgcn_readlane(own.len, who);
-      q.tiles = __builtin_amdgcn_readlane(own.tiles, who);
-      q.u0 = __builtin_amdgcn_readlane(own.u0, who);
-      q.nb = __builtin_amdgcn_readlane(own.nb, who);
-      seq_base = __builtin_amdgcn_readlane(upto, who) - q.tiles * s.kv_heads * (k ? k : q.nb);
+      const Seq& at = seqs[who];
+      q.first = __builtin_amdgcn_readfirstlane(at.first);
+      q.n = __builtin_amdgcn_readfirstlane(at.n);
+      q.len = __builtin_amdgcn_readfirstlane(at.len);
+      q.tiles = __builtin_amdgcn_readfirstlane(at.tiles);
+      q.u0 = __builtin_amdgcn_readfirstlane(at.u0);
+      q.nb = __builtin_amdgcn_readfirstlane(at.nb);
+      seq_base = __builtin_amdgcn_readfirstlane(uptos[who]) - q.tiles * s.kv_heads * (c ? parts_of(q) : q.nb);
     } else {
       int64_t base;
       pc.seq = find_seq(before, b.n_seqs, x0, weight, base);
@@ -230,21 +272,21 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
     }
     const int nb = q.nb;
     const count_t local = x0 - seq_base;
-    if (k) {
+    if (c) {
       // a head's pieces one after the other, each for all row tiles
-      const int at = (int)local, c = (nb + k - 1) / k;
-      pc.head = at / (q.tiles * k);
-      const int rest = at - pc.head * (q.tiles * k);
+      const int at = (int)local;
+      pc.parts = parts_of(q);
+      pc.head = at / (q.tiles * pc.parts);
+      const int rest = at - pc.head * (q.tiles * pc.parts);
       pc.part = rest / q.tiles;
       pc.tile = rest - pc.part * q.tiles;
-      pc.parts = (nb + c - 1) / c;
-      pc.ub = pc.part * c;
-      pc.take = min(c, nb - pc.ub);
+      const int per = (nb + pc.parts - 1) / pc.parts;
+      pc.ub = pc.part * per;
+      pc.take = min(per, nb - pc.ub);
       pc.counter = me - pc.part * q.tiles;
       pc.slot0 = 2 * pc.counter;
       pc.step = 2 * q.tiles;
       pc.slot1 = pc.slot0 + pc.step;
-      if (pc.take <= 0) return;
     } else {
       const count_t item = quotient(local, (count_t)nb);
       pc.ub = (int)(local - item * nb);
@@ -261,6 +303,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
       pc.head = (int)quotient(item, (count_t)q.tiles);
       pc.tile = (int)(item - (count_t)pc.head * q.tiles);
     }
+    kept = pc;  // for the join; every wave the same
     const int rows_n = q.n * group, start = q.len - q.n;
     const int rows = min(kRows, rows_n - pc.tile * kRows);  // rows of the tile
 
@@ -455,6 +498,12 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
     l = join32(join16(l, sum2), sum2);
 
     // ---- the waves' results joined
+    pc.part = __builtin_amdgcn_readfirstlane(kept.part);
+    pc.parts = __builtin_amdgcn_readfirstlane(kept.parts);
+    pc.counter = __builtin_amdgcn_readfirstlane(kept.counter);
+    pc.slot0 = __builtin_amdgcn_readfirstlane(kept.slot0);
+    pc.slot1 = __builtin_amdgcn_readfirstlane(kept.slot1);
+    pc.step = __builtin_amdgcn_readfirstlane(kept.step);
     if (kb == 0) {
       msh[wave][n] = m;
       lsh[wave][n] = l;
@@ -607,7 +656,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
         if (past) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
       }
     }
-    if (k) return;
+    if (c) return;
     __syncthreads();  // the shared arrays are free for the next piece
     x0 += pc.take;
   }

@@ -329,8 +329,12 @@ def test_attention_matches_the_definition(torch, H, G, D, page, asym, lens, new,
 
 
 SPLITS = [  # the ways a call is cut: H, G, D, page, asym, lens, new, window
-    # one long sequence among short ones: runs that cross items
+    # pieces of one size for uneven lengths
     (8, 8, 64, 16, False, [30] * 9 + [4100] + [25] * 15, None, 0),
+    (8, 8, 128, 64, True, [3000, 900, 100, 1500, 2100, 1, 640, 1300, 2900, 40, 1900, 2500], None, 0),
+    # more items than workgroups: runs that cross items
+    (8, 8, 64, 16, False, [30 + 53 * i % 700 for i in range(40)], None, 0),
+    (8, 8, 128, 16, True, [1 + 97 * i % 900 for i in range(34)], [1 + i % 2 for i in range(34)], 500),
     # more than 64 sequences: one token, a few, many rows of 128 and of 256 an item
     (8, 4, 64, 16, True, [1 + 37 * i % 300 for i in range(70)], None, 0),
     (4, 2, 128, 16, False, [40 + 11 * i % 200 for i in range(66)], [1 + i % 3 for i in range(66)], 50),
