@@ -153,7 +153,11 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  *   out  bf16 [tokens][q_heads][head_dim], must not overlap q
  *   lse  fp32 [tokens][q_heads], or NULL
  * Keys meet q exactly and products and sums are held in fp32; a probability
- * and a value are rounded to fp16 on their way (2^-11 relative each).
+ * and a value are rounded to fp16 on their way (2^-11 relative each), whatever
+ * the scales of other tokens: a probability times its value's scale is off by no
+ * more than 2^-11 of itself or, in calls of many rows, 2^-27 of the row's largest
+ * such product, in calls of few 2^-38 of its largest probability times its
+ * largest scale, if that is more.
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
  * positive and at most 2^64.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.

@@ -11,16 +11,17 @@
 // ahead and write them to LDS as fp16 matrix operands, so that the codes are
 // unpacked once per item and tile: keys as c - z, exact; values as
 // (c - z) s 2^-e with e the exponent of the block's largest scale, rounded
-// once (2^-11).  Two waves share a SIMD, w and w + 4; the first stages the next
-// tile before its own work on this one, so that its matrix steps meet the
-// other's vector work (staging by all eight waves, half a block each, before
-// their work: 817 us for prompts of 4096 tokens with 64 heads of 128, by waves
-// 4-7 after theirs: 812, so: 785 on the same card).  Items of 128 rows
-// leave the staging to waves 0-3 alone, two tiles ahead, and the rows to waves
-// 4-7: such calls read the cache more often per row, and waited for it (8 chats
-// of 72 rows behind 4096 tokens: two workgroups of four waves a compute unit
-// 45 us, this one 42, with the cut by the items that there are and all waves
-// joining 35).
+// once (2^-11), or, where that scale is more than 16 times the block's smallest,
+// as c - z, whose scale the probability takes.  Two waves share a SIMD, w and
+// w + 4; the first stages the next tile before its own work on this one, so that
+// its matrix steps meet the other's vector work (staging by all eight waves, half
+// a block each, before their work: 817 us for prompts of 4096 tokens with 64
+// heads of 128, by waves 4-7 after theirs: 812, so: 785 on the same card).
+// Items of 128 rows leave the staging to waves 0-3 alone, two tiles ahead, and
+// the rows to waves 4-7: such calls read the cache more often per row, and
+// waited for it (8 chats of 72 rows behind 4096 tokens: two workgroups of four
+// waves a compute unit 45 us, this one 42, with the cut by the items that there
+// are and all waves joining 35).
 //
 // Scores.  S^T = K q^T (32x32x16): a lane holds one row and, with key row
 // bits 2 and 3 exchanged when the tile is written, runs of 8 consecutive
@@ -29,12 +30,15 @@
 // 2^15): bf16 has 8 significant bits and fp16 eleven, so an element is exact
 // unless it is below 2^-29 of the largest, and then off by at most 2^-39 of
 // it.  A row's probabilities are w = 2^(score + e - M), rounded to fp16
-// (2^-11); the sum l takes w 2^-e in fp32.  The reference M is the largest
-// score plus its block's e up to some tile and stays there until a lane's
-// eight w add up to more than 2^14 (fp16 holds up to 2^16), so most tiles
-// need no maximum: their w are taken at once, and again, against a new M,
-// where the sum says so (a maximum per tile: 801 and 164 us for prompts of
-// 4096 and a chunk of 512 tokens, so: 789 and 159 us).
+// (2^-11); the sum l takes w 2^-e in fp32.  The reference M is 2^7 below the
+// largest score plus its block's e up to some tile and stays there until a lane's
+// eight w add up to more than fp16 holds, so most tiles need no maximum: their w
+// are taken at once, and again, against a new M, where the sum says so (a
+// maximum per tile: 801 and 164 us for prompts of 4096 and a chunk of 512
+// tokens, so: 789 and 159 us).  In a block of scales far apart a token counts
+// with its own exponent and only for rows that see it, so that no row depends on
+// the scales of tokens without weight in it: fp16's smallest step is 2^-26 of the
+// row's largest product of probability and scale, below the error of O's fp32 sum.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
 // steps and takes about 4500 (prompts of 4096 tokens 764-783 us, 890 TFLOP/s).
@@ -65,7 +69,10 @@ constexpr int kTileMaxSplits = 32;
 constexpr int kMinTiles = 4;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr float kNever = -3e38f;  // M before any score: below any, and finite
-constexpr float kMostSum = 0x1p14f;  // of a lane's eight weights: above it M is raised
+constexpr float kBelow = 7.f;        // M stands this far below the largest score plus e
+constexpr float kApart = 3e38f;      // an exponent that leaves no sum of weights below kMostSum
+constexpr float kMostSum = 65504.f;  // of a lane's eight weights, fp16's largest: above it M is raised
+constexpr float kAlike = 16.f;       // ratio of a block's value scales that takes them apart
 
 // One tile as operands.  Rows are padded by 16 bytes, so that eight
 // consecutive lanes' 16-byte reads meet different banks and every offset is a
@@ -75,7 +82,9 @@ struct Staged {
   uint16_t k[kTileTokens][D + 8];  // row: token with bits 2 and 3 exchanged
   uint16_t v[D][kTileTokens + 8];
   float ks[kTileTokens];       // key scale times softmax scale and log2 e, over q's power of two
-  float e[4];                  // exponents of the four blocks' value scales
+  float e[4];                  // exponents of the four blocks' value scales, or kApart
+  float ea[4];                 // where it is that, their exponents, and their
+  float vf[kTileTokens];       // scales over 2^ea, which are not in v
 };
 
 // A thread's part of a tile on its way from the cache.
@@ -295,42 +304,76 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
           if (bad || j + 1 < item_lo || j + 1 > item_hi) vs[i] &= 0x0000FFFFu;
         }
       }
-      uint32_t mp = vs[0];
+      // largest and smallest, in pairs
+      uint32_t mx[kPairs], mn[kPairs];
       #pragma unroll
-      for (int i = 1; i < kPairs; ++i) mp = max_pairs(mp, vs[i]);
-      if constexpr (D == 64) mp = max_pairs(mp, (uint32_t)__shfl_xor((int)mp, 1, 64));
+      for (int i = 0; i < kPairs; ++i) mx[i] = mn[i] = vs[i];
+      #pragma unroll
+      for (int w = kPairs / 2; w > 0; w /= 2)
+        #pragma unroll
+        for (int i = 0; i < w; ++i) {
+          mx[i] = max_pairs(mx[i], mx[i + w]);
+          mn[i] = min_pairs(mn[i], mn[i + w]);
+        }
+      if constexpr (D == 64) {
+        mx[0] = max_pairs(mx[0], (uint32_t)__shfl_xor((int)mx[0], 1, 64));
+        mn[0] = min_pairs(mn[0], (uint32_t)__shfl_xor((int)mn[0], 1, 64));
+      }
+      const uint32_t most = max(mx[0] & 0xFFFFu, mx[0] >> 16);
+      const uint32_t least = min(mn[0] & 0xFFFFu, mn[0] >> 16);
       // every scale is below 2^e; at most 2^14, so that 2^-e is an fp16 value
-      const int e = (int)((max(mp & 0xFFFFu, mp >> 16) & 0x7FFFu) >> 10) - 14;
-      const uint32_t unit = pack_f16(__builtin_amdgcn_ldexpf(1.f, -e), __builtin_amdgcn_ldexpf(1.f, -e));
+      const int e = (int)((most & 0x7FFFu) >> 10) - 14;
       if (lane == 0) to.e[part] = (float)e;
-      #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {  // 8 tokens: one chunk of two dimensions
-        f16x2 z[4], sg[4];  // less the zero-point: before the scale, or with it for 8
-        const auto value = [](uint32_t c, f16x2 z, f16x2 sg) {
-          if constexpr (ZEROS) return as_u32((as_f16x2(c) + z) * sg);
-          else return as_u32(__builtin_elementwise_fma(as_f16x2(c), sg, z));
-        };
+      const auto put = [&](uint32_t unit, auto apart) {
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sg[j] = as_f16x2(vs[4 * i + j]) * as_f16x2(unit);
-          z[j] = sg[j] * as_f16x2(0xC800C800u);  // -8 of them, exact
+        for (int i = 0; i < D / 64; ++i) {  // 8 tokens: one chunk of two dimensions
+          f16x2 z[4], sg[4];  // less the zero-point: before the scale, or with it for 8
+          const auto value = [](uint32_t c, f16x2 z, f16x2 sg) {
+            if constexpr (ZEROS) return as_u32((as_f16x2(c) + z) * sg);
+            else return as_u32(__builtin_elementwise_fma(as_f16x2(c), sg, z));
+          };
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sg[j] = decltype(apart)::value ? as_f16x2(unit) : as_f16x2(vs[4 * i + j]) * as_f16x2(unit);
+            z[j] = sg[j] * as_f16x2(0xC800C800u);  // -8 of them, exact
+          }
+          if constexpr (ZEROS) {
+            const uint32_t a0 = high_codes(fe.vz[2 * i]) | 0x80808080u;
+            const uint32_t a1 = high_codes(fe.vz[2 * i + 1]) | 0x80808080u;
+            z[0] = as_f16x2(f16_01(a0));
+            z[1] = as_f16x2(f16_23(a0));
+            z[2] = as_f16x2(f16_01(a1));
+            z[3] = as_f16x2(f16_23(a1));
+          }
+          #pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const uint32_t w0 = odd ? high_codes(fe.v[2 * i]) : low_codes(fe.v[2 * i]);
+            const uint32_t w1 = odd ? high_codes(fe.v[2 * i + 1]) : low_codes(fe.v[2 * i + 1]);
+            const u32x4 c = {value(f16_01(w0), z[0], sg[0]), value(f16_23(w0), z[1], sg[1]),
+                             value(f16_01(w1), z[2], sg[2]), value(f16_23(w1), z[3], sg[3])};
+            *reinterpret_cast<u32x4*>(&to.v[2 * col + odd][16 * part + 8 * (i + half_col)]) = c;
+          }
         }
-        if constexpr (ZEROS) {
-          const uint32_t a0 = high_codes(fe.vz[2 * i]) | 0x80808080u;
-          const uint32_t a1 = high_codes(fe.vz[2 * i + 1]) | 0x80808080u;
-          z[0] = as_f16x2(f16_01(a0));
-          z[1] = as_f16x2(f16_23(a0));
-          z[2] = as_f16x2(f16_01(a1));
-          z[3] = as_f16x2(f16_23(a1));
+      };
+      put(pack_f16(__builtin_amdgcn_ldexpf(1.f, -e), __builtin_amdgcn_ldexpf(1.f, -e)), std::false_type{});
+      // Scales far apart (a slot that counts as 0 makes them so, at an edge): the
+      // values again, without them.  Tested behind the stores that nearly every
+      // block needs alone (prompts of 4096 tokens 803 us; before them 808, and
+      // without the test 790).
+      if (__builtin_amdgcn_readfirstlane(half_bits_to_f32((uint16_t)most) >
+                                         kAlike * half_bits_to_f32((uint16_t)least))) {
+        put(0x3C003C00u, std::true_type{});
+        if (lane == 0) {
+          to.e[part] = kApart;
+          to.ea[part] = (float)e;
         }
-        #pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {
-          const uint32_t w0 = odd ? high_codes(fe.v[2 * i]) : low_codes(fe.v[2 * i]);
-          const uint32_t w1 = odd ? high_codes(fe.v[2 * i + 1]) : low_codes(fe.v[2 * i + 1]);
-          const u32x4 c = {value(f16_01(w0), z[0], sg[0]), value(f16_23(w0), z[1], sg[1]),
-                           value(f16_01(w1), z[2], sg[2]), value(f16_23(w1), z[3], sg[3])};
-          *reinterpret_cast<u32x4*>(&to.v[2 * col + odd][16 * part + 8 * (i + half_col)]) = c;
-        }
+        if (lane <= half_col)  // a lane for each of the block's tokens
+          #pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            float* f = &to.vf[16 * part + 8 * half_col + 2 * i];
+            f[0] = __builtin_amdgcn_ldexpf(half_bits_to_f32((uint16_t)vs[i]), -e);
+            f[1] = __builtin_amdgcn_ldexpf(half_bits_to_f32((uint16_t)(vs[i] >> 16)), -e);
+          }
       }
     }
   };
@@ -380,8 +423,13 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     const int j = j0 + 16 * g + 8 * half + r;
     return j < lo || j > hi;
   };
+  // Their value scales over 2^e where these are not in the values.
+  const auto value_scale = [&](const Staged<D>& st, int g, f32x4 (&f)[2]) {
+    f[0] = *reinterpret_cast<const f32x4*>(&st.vf[16 * g + 8 * half]);
+    f[1] = *reinterpret_cast<const f32x4*>(&st.vf[16 * g + 8 * half + 4]);
+  };
   // Probabilities against M as it is, and their sums by group.
-  const auto weights = [&](auto edge, const Staged<D>& st, f32x4 eb, int j0, f32x4& sums) {
+  const auto weights = [&](const Staged<D>& st, f32x4 eb, f32x4& sums) {
     #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const float ref = m - eb[g];
@@ -391,32 +439,57 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
       #pragma unroll
       for (int r = 0; r < 8; r += 2) {
         const int at = 8 * (g & 1) + r;
-        float w0 = fast_exp2(fmaf(sc[g >> 1][at], k[r >> 2][r & 3], -ref));
-        float w1 = fast_exp2(fmaf(sc[g >> 1][at + 1], k[r >> 2][(r & 3) + 1], -ref));
-        if constexpr (decltype(edge)::value) {
-          if (hidden(j0, g, r)) w0 = 0.f;
-          if (hidden(j0, g, r + 1)) w1 = 0.f;
-        }
+        const float w0 = fast_exp2(fmaf(sc[g >> 1][at], k[r >> 2][r & 3], -ref));
+        const float w1 = fast_exp2(fmaf(sc[g >> 1][at + 1], k[r >> 2][(r & 3) + 1], -ref));
         sum += w0 + w1;
         pf[g][r >> 1] = pack_f16(w0, w1);
       }
       sums[g] = sum;
     }
   };
-  // M becomes the largest score so far (plus e).
-  const auto raise = [&](const Staged<D>& st, f32x4 eb, int j0) {
-    float mn = m;
+  // The same of group g with tokens that the row does not see, and, in a block
+  // of scales far apart, times its token's.
+  const auto weights_of = [&](auto apart, int g, const Staged<D>& st, float e, int j0) {
+    const float ref = m - e;
+    f32x4 k[2], f[2];
+    key_scale(st, g, k);
+    if constexpr (decltype(apart)::value) value_scale(st, g, f);
+    float sum = 0.f;
     #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      f32x4 k[2];
-      key_scale(st, g, k);
-      #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float x = fmaf(sc[g >> 1][8 * (g & 1) + r], k[r >> 2][r & 3], eb[g]);
-        if (!hidden(j0, g, r)) mn = fmaxf(mn, x);
+    for (int r = 0; r < 8; r += 2) {
+      const int at = 8 * (g & 1) + r;
+      float w0 = fast_exp2(fmaf(sc[g >> 1][at], k[r >> 2][r & 3], -ref));
+      float w1 = fast_exp2(fmaf(sc[g >> 1][at + 1], k[r >> 2][(r & 3) + 1], -ref));
+      if (hidden(j0, g, r)) w0 = 0.f;
+      if (hidden(j0, g, r + 1)) w1 = 0.f;
+      sum += w0 + w1;
+      if constexpr (decltype(apart)::value) {
+        w0 *= f[r >> 2][r & 3];
+        w1 *= f[r >> 2][(r & 3) + 1];
       }
+      pf[g][r >> 1] = pack_f16(w0, w1);
     }
-    mn = join32(mn, larger);
+    return sum;
+  };
+  // Largest score of group g plus e, there of the token's own scale.
+  const auto largest_of = [&](auto apart, int g, const Staged<D>& st, float e, int j0) {
+    f32x4 k[2], f[2];
+    key_scale(st, g, k);
+    if constexpr (decltype(apart)::value) value_scale(st, g, f);
+    float top = kNever;
+    #pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      float own = e;
+      if constexpr (decltype(apart)::value)
+        own += (float)(__builtin_amdgcn_frexp_expf(f[r >> 2][r & 3]) - 1);
+      const float x = fmaf(sc[g >> 1][8 * (g & 1) + r], k[r >> 2][r & 3], own);
+      if (!hidden(j0, g, r)) top = fmaxf(top, x);
+    }
+    return top;
+  };
+  // M becomes the largest so far less kBelow.
+  const auto raise = [&](float top) {
+    const float mn = fmaxf(m, join32(top, larger) - kBelow);
     const float alpha = fast_exp2(m - mn);
     l *= alpha;
     #pragma unroll
@@ -424,18 +497,33 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     m = mn;
   };
   const auto softmax = [&](const Staged<D>& st, int j0) {
-    const f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
-    const bool edge = j0 < all_lo || j0 + kTileTokens - 1 > all_hi;
+    f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
     f32x4 sums;
     bool done = false;
-    if (!edge) {
-      weights(std::false_type{}, st, eb, j0, sums);
+    if (j0 >= all_lo && j0 + kTileTokens - 1 <= all_hi) {
+      weights(st, eb, sums);
       const float most = fmaxf(fmaxf(sums[0], sums[1]), fmaxf(sums[2], sums[3]));
       done = !__any(most > kMostSum);
     }
     if (!done) {
-      raise(st, eb, j0);
-      weights(std::true_type{}, st, eb, j0, sums);
+      const std::true_type apart;
+      const std::false_type alike;
+      bool is_apart[4];
+      float top = kNever;
+      #pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        is_apart[g] = __builtin_amdgcn_readfirstlane(__float_as_int(eb[g])) == __float_as_int(kApart);
+        if (is_apart[g]) {
+          eb[g] = st.ea[g];
+          top = fmaxf(top, largest_of(apart, g, st, eb[g], j0));
+        } else {
+          top = fmaxf(top, largest_of(alike, g, st, eb[g], j0));
+        }
+      }
+      raise(top);
+      #pragma unroll
+      for (int g = 0; g < 4; ++g)
+        sums[g] = is_apart[g] ? weights_of(apart, g, st, eb[g], j0) : weights_of(alike, g, st, eb[g], j0);
     }
     #pragma unroll
     for (int g = 0; g < 4; ++g) l += __builtin_amdgcn_ldexpf(sums[g], -(int)eb[g]);

@@ -1,0 +1,184 @@
+"""The key/value cache over the whole range of what it may hold: value scales
+far apart within a block of 16 tokens (needs an MI355X).
+
+Attention is held to what include/spear_ec_kv.h states, with u = 2^-24,
+p_j = exp(S_j - m) / l, s_j the value's scale and v_j its codes less z:
+  * a score is a sum of D products of q with codes up to 15, less z times the
+    sum of q, in fp32, and a few products: |dS| <= (D + 16) u scale s 30 sum|q|;
+    p_j is off by twice the largest dS and by exp's and its argument's rounding,
+    under 2^-18;
+  * a probability and a value are rounded to fp16, 2^-11 of themselves each:
+    2^-10 + 2^-22 together;
+  * O's sum, in fp32, runs over products with codes and zero-points up to 15
+    apart: (n / 16 + 64) u 30 sum p_j s_j.  In calls of many rows a p_j s_j is
+    also no finer than 2^-27 of the row's largest, which n times 15 of that, at
+    most n / 8 * 15 u, stays below;
+  * in calls of few rows a p_j s_j is no finer than 2^-38 of the row's largest
+    p_j times its largest s_j;
+  * the output is rounded once to bf16.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import kv_reference as ref
+import quantization_error_compensation_amd as q
+from test_gpu_kv import Case, note, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def expected(c, few, scale=None, window=0):
+    """(out, lse, tolerance of out, of lse) of a case, by the definition."""
+    scale = c.D ** -0.5 if scale is None else scale
+    x = ref.bf16_to_f64(c.q)
+    T, H, D = x.shape
+    out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
+    tol, ltol = np.zeros((T, H, D)), np.zeros((T, H))
+    R = H // c.G
+    for b, length in enumerate(c.lens):
+        n = int(c.offsets[b + 1] - c.offsets[b])
+        real = np.arange(max(0, n - length), n)          # rows that are no padding
+        pos = length - n + real[:, None]
+        j = np.arange(length)
+        seen = (j <= pos) & (j > pos - window if window else True)
+        seen = np.repeat(seen, R, 0)
+        for g in range(c.G if len(real) else 0):
+            kc, ks = c.cache.parts(c.table[b], length, g, 0)
+            vc, vs = c.cache.parts(c.table[b], length, g, 1)
+            rows = np.ix_(c.offsets[b] + real, np.arange(g * R, (g + 1) * R))
+            xr = x[rows].reshape(-1, D)
+            with np.errstate(invalid="ignore", over="ignore"):
+                S = np.where(seen, (xr @ kc.T) * ks * scale, -np.inf)
+                top = S.max(1)
+                e = np.exp(S - top[:, None])
+            l = e.sum(1)
+            p = e / l[:, None]
+            pv = p * vs
+            o = pv @ vc
+            ls = top + np.log(l)
+            dS = scale * np.where(seen, ks, 0).max(1) * (D + 16) * ref.U * 30 * np.abs(xr).sum(1)
+            second = np.partition(S, -2, 1)[:, -2] if length > 1 else np.full(len(S), -np.inf)
+            # one token has all the weight whatever the scores' errors: p is 1 and 0
+            dp = np.where(top - second - 2 * dS > 100, 0.0, 2 * dS)[:, None]
+            t = ((dp + 2.0 ** -10 + 2.0 ** -22 + 2.0 ** -18) * (pv @ np.abs(vc))
+                 + ((seen.sum(1) / 16 + 64) * ref.U * 30 * pv.sum(1))[:, None])
+            if few:
+                t += ((2.0 ** -38 * p.max(1) * np.where(seen, vs, 0).max(1))[:, None]
+                      * (seen.astype(float) @ np.abs(vc)))
+            t += ref.half_step_bf16(np.abs(o) + t)
+            shape = (len(real), R)
+            out[rows], tol[rows] = o.reshape(*shape, D), t.reshape(*shape, D)
+            lse[rows], ltol[rows] = ls.reshape(shape), (dS + 2.0 ** -20 * (1 + np.abs(ls))).reshape(shape)
+    return out, lse, tol, ltol
+
+
+def check(c, out, lse, few, skip=(), scale=None, window=0):
+    ro, rl, tol, ltol = expected(c, few, scale, window)
+    o = ref.bf16_to_f64(out.view(c.torch.int16).cpu().numpy().view(np.uint16))
+    v = lse.cpu().numpy().astype(np.float64)
+    keep = [t for t in range(int(c.offsets[-1])) if t not in skip]
+    assert np.isfinite(o[keep]).all(), "output not finite"
+    err = np.abs(o - ro)[keep]
+    worst = (err - tol[keep]).max()
+    assert worst <= 0, f"off by {worst:.3g} more than allowed"
+    none = np.isneginf(rl[keep])
+    assert np.array_equal(np.isneginf(v[keep]), none)
+    e = np.abs(v[keep] - np.where(none, 0, rl[keep]))[~none] - ltol[keep][~none]
+    assert e.size == 0 or e.max() <= 0, f"lse off by {e.max():.3g} more than allowed"
+
+
+# ------------------------------------------------------------ value scales
+CALLS = [  # H, G, D, page, asym, lens, new, window, few rows' kernel
+    (8, 2, 64, 16, True, [90, 33], [3, 2], 0, True),
+    (4, 1, 128, 16, False, [70, 20], [6, 20], 0, True),
+    (8, 1, 128, 16, False, [40, 90], [40, 40], 0, False),     # 128 rows an item
+    (8, 1, 64, 32, True, [130], [70], 50, False),
+    (16, 1, 128, 16, True, [1100], [17], 0, False),           # cut into runs
+    (32, 32, 64, 16, False, [130, 131], [130, 131], 0, False),  # 256 rows an item
+    (32, 32, 128, 64, True, [140, 130], [130, 130], 70, False),
+]
+
+
+def scales(kind):
+    def later(n):               # a larger one that the block's first rows do not see
+        s = np.full(n, 2.0 ** -14)
+        s[5::16] = 2.0 ** 12
+        return s
+
+    def ratios(n):              # two scales a block, 1 to 26 powers of two apart
+        s = np.full(n, 2.0 ** -12)
+        at = np.arange(n)
+        s[at % 16 == 11] *= 2.0 ** (1 + at[at % 16 == 11] // 16 % 26)
+        return s
+
+    def wild(n):                # every fp16 exponent, subnormal scales among them
+        return np.exp2(np.random.default_rng(n).uniform(-24, 15.9, n))
+
+    def blocks(n):              # alike in a block, far apart from block to block
+        r = np.random.default_rng(n)
+        return np.exp2(r.uniform(-14, 12, n // 16 + 1))[np.arange(n) // 16] * r.uniform(0.3, 1, n)
+    return {"later": later, "ratios": ratios, "wild": wild, "blocks": blocks}[kind]
+
+
+@pytest.mark.parametrize("kind", ["later", "ratios", "wild", "blocks"])
+@pytest.mark.parametrize("H,G,D,page,asym,lens,new,window,few", CALLS)
+def test_value_scales_far_apart(torch, H, G, D, page, asym, lens, new, window, few, kind):  # noqa: F811
+    note(f"scales {kind} H={H} G={G} D={D} asym={asym} lens={lens} new={new} window={window}")
+    c = Case(torch, H, G, D, page, asym, lens, new, seed=D + H).fill(value_scales=scales(kind))
+    out, lse, ws = c.attend(window=window)
+    check(c, out, lse, few, window=window)
+    again, lse2, _ = c.attend(window=window, ws=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2), "the same call differs"
+
+
+@pytest.mark.parametrize("bits", [13, 20, 26])
+@pytest.mark.parametrize("H,G,D,page,asym,lens,new,window,few", CALLS)
+def test_value_scales_that_no_weight_meets(torch, H, G, D, page, asym, lens, new, window, few, bits):  # noqa: F811
+    """Every fifth token has scales 2^bits times the others' and scores so low that its weight is
+    nothing (2^-40 and less): the row is its neighbours' alone."""
+    note(f"scales without weight 2^{bits} H={H} G={G} D={D} asym={asym} lens={lens} new={new}")
+
+    def vs(n):
+        s = np.full(n, 2.0 ** -14)
+        s[2::5] *= 2.0 ** bits
+        return s
+
+    c = Case(torch, H, G, D, page, asym, lens, new, seed=D + bits)
+    c.q = ref.f64_to_bf16(1 + 0.3 * c.rng.standard_normal((c.rows, H, D)))
+    c.fill(value_scales=vs)
+    for b, n in enumerate(lens):
+        for g in range(G):
+            codes, s = c.cache.parts(c.table[b], n, g, 0)
+            for t in range(2, n, 5):
+                c.cache.put(c.table[b], t, g, 0, np.zeros(D, np.uint8), np.float16(1.0).view(np.uint16),
+                            15 if asym else 8)
+    c.upload()
+    out, lse, _ = c.attend(window=window)
+    check(c, out, lse, few, window=window)
+
+
+@pytest.mark.parametrize("H,G,D,page,asym,lens,new,window,few", CALLS)
+def test_vectors_of_zeros_beside_small_values(torch, H, G, D, page, asym, lens, new, window, few):  # noqa: F811
+    """As the append stores them: a vector of zeros has scale 1, whatever stands next to it."""
+    note(f"zeros beside small values H={H} G={G} D={D} asym={asym} lens={lens} new={new}")
+    c = Case(torch, H, G, D, page, asym, lens, lens, seed=D)
+    c.upload()
+    kv = c.rng.standard_normal((c.rows, 2 * G, D))
+    kv[:, G:] *= 1e-3
+    kv[3::7, G:] = 0
+    bits = ref.f64_to_bf16(kv)
+    d = c.bf16(bits)
+    q.spear_ec_kv_append(c.desc, c.batch, None, d[:, :G], d[:, G:], None, c.codes, c.scales, c.zeros, None)
+    ref.append(c.cache, np.zeros((c.rows, H, D), np.uint16), bits[:, :G], bits[:, G:], c.offsets, lens, c.table)
+    torch.cuda.synchronize()
+    assert np.array_equal(c.codes.cpu().numpy(), c.cache.codes)
+    c.new = list(new)
+    c.offsets = np.concatenate([[0], np.cumsum(new)]).astype(int)
+    c.rows = int(c.offsets[-1])
+    c.q = c.q[:c.rows]
+    c.d_offsets = c.dev(c.offsets.astype(np.int32))
+    c.batch = q.make_kv_batch(c.d_offsets, c.d_lens, c.d_table, c.rows)
+    out, lse, _ = c.attend(window=window)
+    check(c, out, lse, few, window=window)
