@@ -152,12 +152,14 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  *   q    bf16, row t at t * q_stride elements, [q_heads][head_dim] in a row
  *   out  bf16 [tokens][q_heads][head_dim], must not overlap q
  *   lse  fp32 [tokens][q_heads], or NULL
- * Keys meet q exactly and products and sums are held in fp32; a probability
- * and a value are rounded to fp16 on their way (2^-11 relative each), whatever
- * the scales of other tokens: a probability times its value's scale is off by no
- * more than 2^-11 of itself or, in calls of many rows, 2^-27 of the row's largest
- * such product, in calls of few 2^-38 of its largest probability times its
- * largest scale, if that is more.
+ * Keys meet q exactly, but for elements below 2^-19 of their row's largest in
+ * calls of many rows, which are off by at most 2^-27 of it; products and sums are
+ * held in fp32.  A probability and a value are rounded to fp16 on their way
+ * (2^-11 relative each), whatever the scales of other tokens: a probability times
+ * its value's scale is off by no more than 2^-11 of itself or, in calls of many
+ * rows, 2^-27 of the row's largest such product, in calls of few 2^-38 of its
+ * largest probability times its largest scale, if that is more.  Whatever a row of
+ * q holds, the others keep these bounds.
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
  * positive and at most 2^64.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.

@@ -26,10 +26,11 @@
 // Scores.  S^T = K q^T (32x32x16): a lane holds one row and, with key row
 // bits 2 and 3 exchanged when the tile is written, runs of 8 consecutive
 // tokens, which is the operand order that O^T = V^T P^T wants.  q enters as
-// fp16 times one power of two for the item's rows (its largest element below
-// 2^15): bf16 has 8 significant bits and fp16 eleven, so an element is exact
-// unless it is below 2^-29 of the largest, and then off by at most 2^-39 of
-// it.  A row's probabilities are w = 2^(score + e - M), rounded to fp16
+// fp16 times a power of two, one for the item's rows (its largest element below
+// 2^15) unless that leaves a row's largest below 4, which takes its own then and
+// has its scores multiplied: bf16 has 8 significant bits and fp16 eleven, so an
+// element is exact unless it is below 2^-19 of its row's largest, and then off by
+// at most 2^-27 of it.  A row's probabilities are w = 2^(score + e - M), rounded to fp16
 // (2^-11); the sum l takes w 2^-e in fp32.  The reference M is 2^7 below the
 // largest score plus its block's e up to some tile and stays there until a lane's
 // eight w add up to more than fp16 holds, so most tiles need no maximum: their w
@@ -41,7 +42,7 @@
 // row's largest product of probability and scale, below the error of O's fp32 sum.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
-// steps and takes about 4500 (prompts of 4096 tokens 764-783 us, 890 TFLOP/s).
+// steps and takes about 4500 (prompts of 4096 tokens 787-797 us, 860 TFLOP/s).
 // Counters there: matrix cores busy 38% of the time, vector units 50%, LDS 34%:
 // two waves a SIMD, all that 230 registers leave room for, wait for each other's
 // results rather than for one unit (32 fewer vector instructions a tile in the
@@ -105,6 +106,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
   __shared__ int64_t before[SMALL ? 1 : kMaxChunks + 1];
   __shared__ __attribute__((aligned(16))) Staged<D> buf[2];
   __shared__ float red[kWaves];
+  __shared__ float row_factor[kWaves][32];
   __shared__ int flag;
   constexpr int kTileRows = NARROW ? 128 : 256, kRowFloats = D + 2;
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -168,12 +170,12 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
   const int hi = live ? min(pos, capacity - 1) : 0x7FFFFFFF;  // no row: nothing to mask
   const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
   u32x4 qf[D / 16];
-  float big = 0.f;
+  float big = 0.f;  // the row's largest element
   {
     const uint16_t* qp = a.q + (int64_t)(q.first + tok) * a.q_stride + qh * D + 8 * half;
     #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      qf[i] = live ? load16(qp + 16 * i) : u32x4{0, 0, 0, 0};
+      qf[i] = pos >= 0 ? load16(qp + 16 * i) : u32x4{0, 0, 0, 0};  // padding may hold anything
       #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float f0 = fabsf(bf16_lo(qf[i][j])), f1 = fabsf(bf16_hi(qf[i][j]));
@@ -182,13 +184,23 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
       }
     }
   }
+  big = join32(big, larger);
+  float most_q = big;
   #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
-  if (lane == 0) red[wave] = big;
+  for (int o = 16; o > 0; o >>= 1) most_q = fmaxf(most_q, __shfl_xor(most_q, o, 64));
+  if (lane == 0) red[wave] = most_q;
   __syncthreads();
-  for (int i = 0; i < kWaves; ++i) big = fmaxf(big, red[i]);
-  const int qe = min(110, max(-110, 15 - __builtin_amdgcn_frexp_expf(big)));  // big 2^qe < 2^15
-  const float qmul = __builtin_amdgcn_ldexpf(1.f, qe);
+  for (int i = 0; i < kWaves; ++i) most_q = fmaxf(most_q, red[i]);
+  // The item's power of two, and the row's own where the item's does not leave
+  // its largest element between 2^2 and 2^15.  The bounds keep every factor finite
+  // for softmax scales up to 2^64.
+  const int qe = min(60, max(-26, 15 - __builtin_amdgcn_frexp_expf(most_q)));
+  const int at_qe = __builtin_amdgcn_frexp_expf(big) + qe;
+  const int own_qe = big == 0.f || (at_qe >= 3 && at_qe <= 15)
+                         ? qe : min(min(127, qe + 126), max(-113, 15 - __builtin_amdgcn_frexp_expf(big)));
+  const bool scaled = __any(own_qe != qe);
+  row_factor[wave][n] = __builtin_amdgcn_ldexpf(1.f, qe - own_qe);  // the wave's own
+  const float qmul = __builtin_amdgcn_ldexpf(1.f, own_qe);
   #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const u32x4 r = x_permute8(qf[i]);
@@ -500,12 +512,17 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
     f32x4 sums;
     bool done = false;
-    if (j0 >= all_lo && j0 + kTileTokens - 1 <= all_hi) {
+    if (!scaled && j0 >= all_lo && j0 + kTileTokens - 1 <= all_hi) {
       weights(st, eb, sums);
       const float most = fmaxf(fmaxf(sums[0], sums[1]), fmaxf(sums[2], sums[3]));
       done = !__any(most > kMostSum);
     }
     if (!done) {
+      if (scaled) {
+        const float f = row_factor[wave][n];
+        sc[0] *= f;
+        sc[1] *= f;
+      }
       const std::true_type apart;
       const std::false_type alike;
       bool is_apart[4];

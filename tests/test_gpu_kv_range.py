@@ -1,5 +1,6 @@
 """The key/value cache over the whole range of what it may hold: value scales
-far apart within a block of 16 tokens (needs an MI355X).
+far apart within a block of 16 tokens, queries far apart within a call, and
+padding rows of any content (needs an MI355X).
 
 Attention is held to what include/spear_ec_kv.h states, with u = 2^-24,
 p_j = exp(S_j - m) / l, s_j the value's scale and v_j its codes less z:
@@ -182,3 +183,46 @@ def test_vectors_of_zeros_beside_small_values(torch, H, G, D, page, asym, lens, 
     c.batch = q.make_kv_batch(c.d_offsets, c.d_lens, c.d_table, c.rows)
     out, lse, _ = c.attend(window=window)
     check(c, out, lse, few, window=window)
+
+
+# ------------------------------------------------------------ query rows
+@pytest.mark.parametrize("big", [2.0 ** 20, 2.0 ** 34, 2.0 ** 40, 1e30, 3e38])
+@pytest.mark.parametrize("H,G,D,page,asym,lens,new,window,few", CALLS)
+def test_a_large_query_row_stays_alone(torch, H, G, D, page, asym, lens, new, window, few, big):  # noqa: F811
+    """One (token, head) of each sequence is `big` times the others, one token 2^-40 of them: the
+    others' results are theirs alone."""
+    note(f"query row of {big:g} H={H} G={G} D={D} lens={lens} new={new}")
+    c = Case(torch, H, G, D, page, asym, lens, new, seed=D + 3).fill()
+    x = ref.bf16_to_f64(c.q)
+    rows = [int(o) + n // 2 for o, n in zip(c.offsets, new)]
+    x[[int(o) + n - 1 for o, n in zip(c.offsets, new)]] *= 2.0 ** -40
+    for t in rows:
+        x[t, H - 1] = np.clip(x[t, H - 1] * big, -3.3e38, 3.3e38)
+    c.q = ref.f64_to_bf16(x)
+    out, lse, _ = c.attend(window=window)
+    ro, rl, tol, ltol = expected(c, few, window=window)
+    o = ref.bf16_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16))
+    v = lse.cpu().numpy().astype(np.float64)
+    keep = np.ones(o.shape[:2], bool)
+    keep[rows, H - 1] = False
+    assert np.isfinite(o[keep]).all() and np.isfinite(v[keep]).all()
+    assert (np.abs(o - ro) - tol)[keep].max() <= 0
+    assert (np.abs(v - rl) - ltol)[keep].max() <= 0
+
+
+@pytest.mark.parametrize("what", [1e30, 3e38, float("inf"), float("nan")])
+@pytest.mark.parametrize("H,G,D,new,few", [(8, 2, 64, 6, True), (8, 1, 128, 40, False),
+                                           (32, 32, 64, 140, False), (32, 32, 128, 140, False)])
+def test_padding_rows_hold_anything(torch, H, G, D, new, few, what):  # noqa: F811
+    """Rows at negative positions: zeros and -inf, and nothing of them in the rows beside them."""
+    note(f"padding of {what} H={H} G={G} D={D} new={new}")
+    c = Case(torch, H, G, D, 16, False, [3, new - 1, new + 9], [new] * 3, seed=D).fill()
+    pad = [t for b, n in enumerate(c.lens) for t in range(c.offsets[b], c.offsets[b] + max(0, new - n))]
+    x = torch.full((c.rows, H, D), what, device="cuda", dtype=torch.bfloat16)
+    keep = [t for t in range(c.rows) if t not in pad]
+    x[keep] = c.bf16(c.q)[keep]
+    c.q[pad] = 0
+    out, lse, ws = c.attend(d_q=x)
+    check(c, out, lse, few)
+    assert (out[pad] == 0).all() and torch.isneginf(lse[pad]).all()
+    assert q.spear_ec_workspace_status(ws) == 0
