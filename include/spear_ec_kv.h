@@ -160,6 +160,9 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  * rows, 2^-27 of the row's largest such product, in calls of few 2^-38 of its
  * largest probability times its largest scale, if that is more.  Whatever a row of
  * q holds, the others keep these bounds.
+ * Scores past 2^23 (in powers of two), whose digits below 1 fp32 does not hold,
+ * decide by the digits that it does; a row whose scores leave fp32 itself may hold
+ * anything.
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
  * positive and at most 2^64.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.

@@ -26,10 +26,11 @@
 // against the same probabilities, subtracted once a unit, so that it never
 // grows with the sequence.  Keys and q meet exactly.  A probability
 // times its value's scale is rounded to fp16 (2^-11 relative, an eighth of the
-// output's bf16 rounding): the running reference M is the rows' maximum score
-// plus the exponent of the largest value scale so far, less 14, so that
-// w = 2^(score - M) s stays below 2^14 and is exact to its 11 bits down to
-// 2^-28 of that.  Every sum is fp32.
+// output's bf16 rounding): the running reference M is the row's maximum score,
+// down to a whole number, plus the exponent of the largest value scale so far,
+// less 14, so that w = 2^(score - M) s stays below 2^15 and is exact to its 11 bits
+// down to 2^-29 of that.  Every sum is fp32.  Scores past 2^23 count times a power
+// of two that brings them below it.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -45,6 +46,7 @@ constexpr int kGroups = 256;     // workgroups: one per compute unit of gfx950
 constexpr int kXcds = 8;         // consecutive workgroups go to them in turn
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
+constexpr float kLarge = 0x1p23f;
 
 template <int D>
 constexpr int slot_floats() { return kRows * D + 2 * kRows; }
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
   if constexpr (SMALL) {
     if (lane < b.n_seqs) own = seq_at(lane);
     const int it = own.tiles * s.kv_heads;
-        upto = wave_prefix(it * own.nb);
+    upto = wave_prefix(it * own.nb);
     items = __builtin_amdgcn_readlane(wave_prefix(it), 63);
     units = __builtin_amdgcn_readlane(upto, 63);
     longest = wave_max(it ? own.nb : 0);
@@ -365,10 +367,11 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
       qf[i] = x_permute8(qf[i]);
     }
     qs = join32(join16(qs, sum2), sum2);
-    const float f = a.scale * kLog2e;  // scores in powers of two
+    float f = a.scale * kLog2e;  // scores in powers of two
 
-    // mx, ev: the row's largest score and value-scale exponent; m: their reference M
-    float mx = -INFINITY, m = -INFINITY, l = 0.f;  // l: the lane's own tokens
+    // mx, ev: the row's largest score, down to a whole number, and value-scale
+    // exponent; M = mx + ev - 28
+    float mx = -INFINITY, l = 0.f;  // l: the lane's own tokens
     int ev = 0;
     f32x4 o[D / 32][2];
     #pragma unroll
@@ -440,19 +443,30 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
       // half bits order like their values, and are denormal floats: joined as integers
       big_s = max(big_s, (uint32_t)__shfl_xor((int)big_s, 16, 64));
       big_s = max(big_s, (uint32_t)__shfl_xor((int)big_s, 32, 64));
-      mx = fmaxf(mx, top * f);
-      ev = max(ev, (int)((big_s & 0x7FFFu) >> 10));
-      const float mn = mx + (float)(ev - 28);  // scale < 2^(ev - 14)
-      if (__any(mn != m)) {
-        const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
+      top *= f;
+      // Past kLarge fp32 leaves a score no digits below 1, and M none for ev: such
+      // a row's scores count times a power of two from here on, which tells two of
+      // them apart where their last digits do.
+      const bool far = fabsf(top) > kLarge && fabsf(top) < INFINITY;
+      if (__any(far)) {
+        const int k = far ? 23 - __builtin_amdgcn_frexp_expf(top) : 0;
+        top = __builtin_amdgcn_ldexpf(top, k);
+        mx = __builtin_amdgcn_ldexpf(mx, k);
+        f = __builtin_amdgcn_ldexpf(f, k);
+      }
+      const float nmx = fmaxf(mx, floorf(top));
+      const int nev = max(ev, (int)((big_s & 0x7FFFu) >> 10));  // scale < 2^(ev - 14)
+      if (__any(nmx != mx || nev != ev)) {
+        const float alpha = fast_exp2((nmx == mx ? 0.f : mx - nmx) + (float)(ev - nev));
         l *= alpha;
         #pragma unroll
         for (int t = 0; t < D / 32; ++t)
           #pragma unroll
           for (int h = 0; h < 2; ++h) o[t][h] *= alpha;
-        m = mn;
+        mx = nmx;
+        ev = nev;
       }
-      const float ref = m == -INFINITY ? 0.f : m;
+      const float ref = mx == -INFINITY ? 0.f : mx + (float)(ev - 28);
       u32x4 pf[4];  // probabilities times value scales, 8 tokens a step
       #pragma unroll
       for (int i = 0; i < 32; i += 2) {
@@ -496,6 +510,8 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
         for (int h = 0; h < 2; ++h) o[t][h] -= off;
     }
     l = join32(join16(l, sum2), sum2);
+    l *= fast_exp2((float)(ev - 28));  // relative to mx from here on
+    mx = __builtin_amdgcn_ldexpf(mx, __builtin_amdgcn_frexp_expf(a.scale * kLog2e) - __builtin_amdgcn_frexp_expf(f));
 
     // ---- the waves' results joined
     pc.part = __builtin_amdgcn_readfirstlane(kept.part);
@@ -505,7 +521,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
     pc.slot1 = __builtin_amdgcn_readfirstlane(kept.slot1);
     pc.step = __builtin_amdgcn_readfirstlane(kept.step);
     if (kb == 0) {
-      msh[wave][n] = m;
+      msh[wave][n] = mx;
       lsh[wave][n] = l;
     }
     __syncthreads();
@@ -513,7 +529,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode_attention_kernel(KvShape s
       float big = msh[0][n];
       #pragma unroll
       for (int w = 1; w < kWaves; ++w) big = fmaxf(big, msh[w][n]);
-      const float kf = m == -INFINITY ? 0.f : fast_exp2(m - big);
+      const float kf = mx == -INFINITY ? 0.f : fast_exp2(mx - big + (float)(ev - 28));
       #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
         // byte columns 16 t + 4 kb + i: eight dimensions in a row

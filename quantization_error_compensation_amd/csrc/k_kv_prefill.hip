@@ -36,13 +36,14 @@
 // eight w add up to more than fp16 holds, so most tiles need no maximum: their w
 // are taken at once, and again, against a new M, where the sum says so (a
 // maximum per tile: 801 and 164 us for prompts of 4096 and a chunk of 512
-// tokens, so: 789 and 159 us).  In a block of scales far apart a token counts
+// tokens, so, before scales and scores were held over their whole range: 789 and
+// 159 us).  In a block of scales far apart a token counts
 // with its own exponent and only for rows that see it, so that no row depends on
 // the scales of tokens without weight in it: fp16's smallest step is 2^-26 of the
 // row's largest product of probability and scale, below the error of O's fp32 sum.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
-// steps and takes about 4500 (prompts of 4096 tokens 787-797 us, 860 TFLOP/s).
+// steps and takes about 4500 (prompts of 4096 tokens 783-785 us, 870 TFLOP/s).
 // Counters there: matrix cores busy 38% of the time, vector units 50%, LDS 34%:
 // two waves a SIMD, all that 230 registers leave room for, wait for each other's
 // results rather than for one unit (32 fewer vector instructions a tile in the
@@ -70,6 +71,7 @@ constexpr int kTileMaxSplits = 32;
 constexpr int kMinTiles = 4;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr float kNever = -3e38f;  // M before any score: below any, and finite
+constexpr float kLarge = 0x1p23f;
 constexpr float kBelow = 7.f;        // M stands this far below the largest score plus e
 constexpr float kApart = 3e38f;      // an exponent that leaves no sum of weights below kMostSum
 constexpr float kMostSum = 65504.f;  // of a lane's eight weights, fp16's largest: above it M is raised
@@ -106,7 +108,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
   __shared__ int64_t before[SMALL ? 1 : kMaxChunks + 1];
   __shared__ __attribute__((aligned(16))) Staged<D> buf[2];
   __shared__ float red[kWaves];
-  __shared__ float row_factor[kWaves][32];
+  __shared__ float row_factor[kWaves][32];  // each wave its own, as is
+  __shared__ int row_shrunk[kWaves][32];
   __shared__ int flag;
   constexpr int kTileRows = NARROW ? 128 : 256, kRowFloats = D + 2;
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -198,8 +201,9 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
   const int at_qe = __builtin_amdgcn_frexp_expf(big) + qe;
   const int own_qe = big == 0.f || (at_qe >= 3 && at_qe <= 15)
                          ? qe : min(min(127, qe + 126), max(-113, 15 - __builtin_amdgcn_frexp_expf(big)));
-  const bool scaled = __any(own_qe != qe);
-  row_factor[wave][n] = __builtin_amdgcn_ldexpf(1.f, qe - own_qe);  // the wave's own
+  bool scaled = __any(own_qe != qe);
+  row_factor[wave][n] = __builtin_amdgcn_ldexpf(1.f, qe - own_qe);
+  row_shrunk[wave][n] = 0;
   const float qmul = __builtin_amdgcn_ldexpf(1.f, own_qe);
   #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
@@ -336,6 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
       // every scale is below 2^e; at most 2^14, so that 2^-e is an fp16 value
       const int e = (int)((most & 0x7FFFu) >> 10) - 14;
       if (lane == 0) to.e[part] = (float)e;
+      const bool far_apart = __any(half_bits_to_f32((uint16_t)most) > kAlike * half_bits_to_f32((uint16_t)least));
       const auto put = [&](uint32_t unit, auto apart) {
         #pragma unroll
         for (int i = 0; i < D / 64; ++i) {  // 8 tokens: one chunk of two dimensions
@@ -369,11 +374,10 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
       };
       put(pack_f16(__builtin_amdgcn_ldexpf(1.f, -e), __builtin_amdgcn_ldexpf(1.f, -e)), std::false_type{});
       // Scales far apart (a slot that counts as 0 makes them so, at an edge): the
-      // values again, without them.  Tested behind the stores that nearly every
-      // block needs alone (prompts of 4096 tokens 803 us; before them 808, and
-      // without the test 790).
-      if (__builtin_amdgcn_readfirstlane(half_bits_to_f32((uint16_t)most) >
-                                         kAlike * half_bits_to_f32((uint16_t)least))) {
+      // values again, without them, behind the stores that are all nearly every
+      // block needs (prompts of 4096 tokens 803 us; with the branch before them
+      // 808; without the test at all 790 then, 771 against 783 now).
+      if (far_apart) {
         put(0x3C003C00u, std::true_type{});
         if (lane == 0) {
           to.e[part] = kApart;
@@ -392,6 +396,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
 
   // M, the lane's own share of l, and O
   float m = kNever, l = 0.f;
+  bool started = false;  // M stands
   f32x16 o[D / 32];
   #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -499,9 +504,10 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     }
     return top;
   };
-  // M becomes the largest so far less kBelow.
+  // M becomes the largest so far less kBelow, a whole number, so that M - e is
+  // exact.
   const auto raise = [&](float top) {
-    const float mn = fmaxf(m, join32(top, larger) - kBelow);
+    const float mn = fmaxf(m, floorf(top - kBelow));
     const float alpha = fast_exp2(m - mn);
     l *= alpha;
     #pragma unroll
@@ -512,7 +518,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     f32x4 eb = *reinterpret_cast<const f32x4*>(st.e);
     f32x4 sums;
     bool done = false;
-    if (!scaled && j0 >= all_lo && j0 + kTileTokens - 1 <= all_hi) {
+    if (started && !scaled && j0 >= all_lo && j0 + kTileTokens - 1 <= all_hi) {
       weights(st, eb, sums);
       const float most = fmaxf(fmaxf(sums[0], sums[1]), fmaxf(sums[2], sums[3]));
       done = !__any(most > kMostSum);
@@ -526,18 +532,34 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
       const std::true_type apart;
       const std::false_type alike;
       bool is_apart[4];
-      float top = kNever;
       #pragma unroll
       for (int g = 0; g < 4; ++g) {
         is_apart[g] = __builtin_amdgcn_readfirstlane(__float_as_int(eb[g])) == __float_as_int(kApart);
-        if (is_apart[g]) {
-          eb[g] = st.ea[g];
-          top = fmaxf(top, largest_of(apart, g, st, eb[g], j0));
-        } else {
-          top = fmaxf(top, largest_of(alike, g, st, eb[g], j0));
-        }
+        if (is_apart[g]) eb[g] = st.ea[g];
+      }
+      const auto largest = [&] {
+        float top = kNever;
+        #pragma unroll
+        for (int g = 0; g < 4; ++g)
+          top = fmaxf(top, is_apart[g] ? largest_of(apart, g, st, eb[g], j0) : largest_of(alike, g, st, eb[g], j0));
+        return join32(top, larger);
+      };
+      float top = largest();
+      const bool far = fabsf(top) > kLarge && fabsf(top) < -kNever;
+      if (__any(far)) {
+        asm volatile("" ::: "memory");  // scales are read again: kept, they took 32 registers
+        const int k = far ? __builtin_amdgcn_frexp_expf(top) - 23 : 0;
+        const float f = __builtin_amdgcn_ldexpf(1.f, -k);
+        sc[0] *= f;
+        sc[1] *= f;
+        if (m != kNever) m *= f;
+        row_factor[wave][n] *= f;
+        row_shrunk[wave][n] += k;
+        scaled = true;
+        top = largest();
       }
       raise(top);
+      started = true;
       #pragma unroll
       for (int g = 0; g < 4; ++g)
         sums[g] = is_apart[g] ? weights_of(apart, g, st, eb[g], j0) : weights_of(alike, g, st, eb[g], j0);
@@ -613,6 +635,17 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     }
   }
   l += __shfl_xor(l, 32, 64);
+  if (scaled) {  // rows of large scores: O over l, M their log-sum
+    const int k = row_shrunk[wave][n];
+    const bool far = k > 0 && l > 0.f;
+    const float inv = far ? 1.f / l : 1.f;
+    if (far) {
+      m = __builtin_amdgcn_ldexpf(m + log2f(l), k);
+      l = 1.f;
+    }
+    #pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= inv;
+  }
 
   if (any_bad && lane == 0) atomicOr(counters + kCtrError, SPEAR_EC_WS_BAD_PAGE);
   // Eight bytes of a row's output and its log-sum; the reciprocal of l.

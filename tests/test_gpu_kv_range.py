@@ -1,6 +1,6 @@
 """The key/value cache over the whole range of what it may hold: value scales
-far apart within a block of 16 tokens, queries far apart within a call, and
-padding rows of any content (needs an MI355X).
+far apart within a block of 16 tokens, queries far apart within a call,
+scores past fp32's integers, and padding rows of any content (needs an MI355X).
 
 Attention is held to what include/spear_ec_kv.h states, with u = 2^-24,
 p_j = exp(S_j - m) / l, s_j the value's scale and v_j its codes less z:
@@ -226,3 +226,22 @@ def test_padding_rows_hold_anything(torch, H, G, D, new, few, what):  # noqa: F8
     check(c, out, lse, few)
     assert (out[pad] == 0).all() and torch.isneginf(lse[pad]).all()
     assert q.spear_ec_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("bits", [20, 24, 30, 40, 90])
+@pytest.mark.parametrize("H,G,D,page,asym,lens,new,window,few", CALLS)
+def test_scores_too_large_for_digits_below_one(torch, H, G, D, page, asym, lens, new, window, few, bits):  # noqa: F811
+    """Rows of 2^bits beside ordinary ones, value scales alike and far apart: where two tokens'
+    scores differ by more than their errors, the larger has all the weight."""
+    note(f"scores of 2^{bits} H={H} G={G} D={D} lens={lens} new={new}")
+    for kind in (None, "wild"):
+        c = Case(torch, H, G, D, page, asym, lens, new, seed=D + bits)
+        c.fill(value_scales=kind and scales(kind))
+        x = ref.bf16_to_f64(c.q)
+        x[::3, ::2] *= 2.0 ** bits
+        x[1::3] -= 2.0 ** (bits - 6)       # of every score far below zero, or far above
+        c.q = ref.f64_to_bf16(x)
+        out, lse, ws = c.attend(window=window)
+        check(c, out, lse, few, window=window)
+        again, lse2, _ = c.attend(window=window, ws=ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2), "the same call differs"
