@@ -247,21 +247,25 @@ __device__ __forceinline__ float element(u32x4 raw, int i) {
   return (i & 1) ? bf16_hi(raw[i / 2]) : bf16_lo(raw[i / 2]);
 }
 
-// The lane's 8 elements rotated: x c + (its pair's other element) s, in fp32
-// with the error of the second product (exact) added back, and in fp64.
-__device__ __forceinline__ void rotate8(float (&f)[8], u32x4 raw, u32x4 other, const Turn& t) {
-  #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = element(other, i), p = y * t.s[i];
-    const float low = __builtin_fmaf(y, t.s[i], -p);
-    f[i] = __builtin_fmaf(element(raw, i), t.c[i], p) + low;
-  }
-}
+// The lane's 8 elements rotated: x c + (its pair's other element) s, in fp64, and
+// in fp32 with the error of the second product (exact) added back.  A product
+// that is infinite has no such error: the result is not to be used then.
 __device__ __forceinline__ void rotate8(double (&f)[8], u32x4 raw, u32x4 other, const Turn& t) {
   #pragma unroll
   for (int i = 0; i < 8; ++i)
     f[i] = __builtin_fma((double)element(raw, i), (double)t.c[i],
                          (double)element(other, i) * (double)t.s[i]);
+}
+__device__ __forceinline__ bool rotate8(float (&f)[8], u32x4 raw, u32x4 other, const Turn& t) {
+  float most = 0.f;
+  #pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = element(other, i), p = y * t.s[i];
+    const float low = __builtin_fmaf(y, t.s[i], -p);
+    f[i] = __builtin_fmaf(element(raw, i), t.c[i], p) + low;
+    most = fmaxf(most, fabsf(p));
+  }
+  return most < INFINITY;
 }
 __device__ __forceinline__ void widen8(float (&x)[8], u32x4 raw) {
   #pragma unroll
@@ -301,7 +305,13 @@ __device__ __forceinline__ void append_queries(const KvShape& s, const KvBatch& 
       o = u32x4{fill, fill, fill, fill};
     } else if (turned) {
       float f[8];
-      rotate8(f, raw[u], partners(raw[u], a.rope, sub), turn);
+      const u32x4 other = partners(raw[u], a.rope, sub);
+      if (!rotate8(f, raw[u], other, turn)) {
+        double d[8];
+        rotate8(d, raw[u], other, turn);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (float)d[e];
+      }
       if (8 * sub < a.rope.dim)
         #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
@@ -321,12 +331,12 @@ __device__ __forceinline__ void store_form(const KvShape& s, const KvRope& rope,
   u32x4 other = {0, 0, 0, 0};
   const bool turned = rope.cos_sin && 8 * sub < rope.dim;
   if (rope.cos_sin) other = partners(kraw, rope, sub);
-  bool k_sure, v_sure;
+  bool k_sure, v_sure, finite = true;
   {
     float x[8];
     widen8(x, kraw);
     if (rope.cos_sin) {
-      if (turned) rotate8(x, kraw, other, turn);
+      if (turned) finite = rotate8(x, kraw, other, turn);
       sk = quantize8<LANES, false>(x, s.zeros, k_sure);
     } else {
       sk = quantize8<LANES, true>(x, s.zeros, k_sure);
@@ -334,7 +344,7 @@ __device__ __forceinline__ void store_form(const KvShape& s, const KvRope& rope,
     widen8(x, vraw);
     sv = quantize8<LANES, true>(x, s.zeros, v_sure);
   }
-  if (__any(!k_sure || !v_sure)) {
+  if (__any(!k_sure || !v_sure || !finite)) {
     double x[8];
     widen8(x, kraw);
     if (turned) rotate8(x, kraw, other, turn);

@@ -1,6 +1,7 @@
 """The key/value cache over the whole range of what it may hold: value scales
 far apart within a block of 16 tokens, queries far apart within a call,
-scores past fp32's integers, and padding rows of any content (needs an MI355X).
+scores past fp32's integers, padding rows of any content, and infinities that
+meet a rotation (needs an MI355X).
 
 Attention is held to what include/spear_ec_kv.h states, with u = 2^-24,
 p_j = exp(S_j - m) / l, s_j the value's scale and v_j its codes less z:
@@ -245,3 +246,71 @@ def test_scores_too_large_for_digits_below_one(torch, H, G, D, page, asym, lens,
         check(c, out, lse, few, window=window)
         again, lse2, _ = c.attend(window=window, ws=ws)
         assert torch.equal(out, again) and torch.equal(lse, lse2), "the same call differs"
+
+
+# ------------------------------------------------------- rotated infinities
+def quantize(x, asym):
+    """ref.quantize for vectors with infinities and NaN: a NaN is no part of the
+    maxima and becomes code 0."""
+    f = np.where(np.isnan(x), 0.0, x)
+    lo, hi = min(0.0, f.min()), max(0.0, f.max())
+    with np.errstate(over="ignore", invalid="ignore"):
+        s = min(np.float16((hi - lo) / 15.0 if asym else max(hi, -lo) / 7.0), np.float16(65504.0))
+        s = s if s != 0 else np.float16(1.0)
+        z = float(np.clip(np.rint(-lo / float(s)), 0, 15)) if asym else 8.0
+        codes = np.clip(np.rint(x / float(s)) + z, 0, 15)
+    return np.where(np.isnan(x), 0, codes).astype(np.uint8), s.view(np.uint16), int(z)
+
+
+@pytest.mark.parametrize("n", [5, 40])          # by rows, and by blocks of positions
+@pytest.mark.parametrize("D,dim", [(64, 64), (128, 128), (128, 48)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("asym", [False, True])
+def test_infinities_that_meet_a_rotation(torch, n, D, dim, inter, asym):  # noqa: F811
+    """Keys and queries with an infinity in either half of a pair, in both, with a NaN, and with
+    values whose products leave fp32 by the table's factors: what 64-bit arithmetic gives."""
+    note(f"rotated infinities n={n} D={D} dim={dim} interleaved={inter} asym={asym}")
+    H, G = 4, 2
+    c = Case(torch, H, G, D, 16, asym, [n + 3], [n], seed=n + D)
+    c.upload()
+    ang = np.outer(np.arange(n + 3), 100.0 ** (-np.arange(dim // 2) / (dim // 2))) + 0.1
+    cs = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+    cs[n // 2 + 3:] *= 1.5                       # tables may carry a factor
+    x = c.rng.standard_normal((n, H + 2 * G, D))
+    a, b = (0, 1) if inter else (0, dim // 2)    # a pair
+    bits = ref.f64_to_bf16(x)
+    inf, ninf, nan, most = 0x7F80, 0xFF80, 0x7FC0, 0x7F7F
+    step = 2 if inter else 1
+    plan = [[(a, inf)], [(b, ninf)], [(a, inf), (b, inf)], [(a, ninf), (b + 2 * step, nan)],
+            [(a + step, most), (b + step, most)]]
+    for t in range(n):
+        for h in range(0, H + G):
+            if (t + h) % 3 == 0:
+                for d, w in plan[(t + h) // 3 % len(plan)]:
+                    bits[t, h, d] = w
+    bits[n - 1, :H + G, a], bits[n - 1, :H + G, b] = most, most     # 3.4e38 times 1.5
+    bits[n - 2, :H + G, a], bits[n - 2, :H + G, b] = most | 0x8000, most
+    d = c.bf16(bits)
+    out = torch.full((n, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    q.spear_ec_kv_append(c.desc, c.batch, d[:, :H], d[:, H:H + G], d[:, H + G:], c.dev(cs), c.codes, c.scales,
+                         c.zeros, out, interleaved=inter)
+    torch.cuda.synchronize()
+    v = ref.bf16_to_f64(bits)
+    got = ref.bf16_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16))
+    for i in range(n):
+        with np.errstate(invalid="ignore"):
+            want = ref.rotate(v[i, :H], 3 + i, cs, dim, inter)
+            kr = ref.rotate(v[i, H:H + G], 3 + i, cs, dim, inter)
+        big = np.abs(want) > 3.3961775e38        # past the largest bf16 and half a step
+        fin = np.isfinite(want) & ~big
+        assert np.array_equal(np.isnan(got[i]), np.isnan(want)), i
+        assert np.array_equal(got[i][np.isinf(want)], want[np.isinf(want)]), i
+        assert (np.isinf(got[i][big]) & (np.sign(got[i][big]) == np.sign(want[big]))).all(), i
+        assert (np.abs(got[i][fin] - want[fin]) <= ref.half_step_bf16(want[fin]) * (1 + 2.0 ** -14)).all(), i
+        for g in range(G):
+            c.cache.put(c.table[0], 3 + i, g, 0, *quantize(kr[g], asym))
+            c.cache.put(c.table[0], 3 + i, g, 1, *quantize(v[i, H + G + g], asym))
+    assert np.array_equal(c.scales.view(torch.int16).cpu().numpy().view(np.uint16), c.cache.scales)
+    assert np.array_equal(c.codes.cpu().numpy(), c.cache.codes)
+    if asym:
+        assert np.array_equal(c.zeros.cpu().numpy(), c.cache.zeros)
