@@ -314,3 +314,26 @@ def test_infinities_that_meet_a_rotation(torch, n, D, dim, inter, asym):  # noqa
     assert np.array_equal(c.codes.cpu().numpy(), c.cache.codes)
     if asym:
         assert np.array_equal(c.zeros.cpu().numpy(), c.cache.zeros)
+
+
+@pytest.mark.parametrize("kind", ["later", "wild"])
+@pytest.mark.parametrize("H,G,D,asym,new,few", [(4, 2, 64, True, 3, True), (8, 2, 128, False, 2, True),
+                                                (8, 1, 64, False, 9, False), (16, 1, 128, True, 10, False),
+                                                (64, 4, 64, True, 17, False), (64, 4, 128, False, 17, False)])
+def test_more_than_64_sequences(torch, H, G, D, asym, new, few, kind):  # noqa: F811
+    """Scales far apart, a large row and garbage in padding, in calls whose lengths do not fit a wave."""
+    note(f"70 sequences {kind} H={H} G={G} D={D} new={new}")
+    lens = [new - 1 if i % 9 == 4 else new + 7 * i % 60 for i in range(70)]
+    c = Case(torch, H, G, D, 16, asym, lens, [new] * 70, seed=D + new).fill(value_scales=scales(kind))
+    pad = [int(c.offsets[b]) for b, n in enumerate(lens) if n < new]
+    x = ref.bf16_to_f64(c.q)
+    x[2 * new - 1::new * 5, 0] *= 2.0 ** 40
+    c.q = ref.f64_to_bf16(x)
+    d_q = c.bf16(c.q)
+    d_q[pad] = 3e38
+    c.q[pad] = 0
+    out, lse, ws = c.attend(d_q=d_q)
+    check(c, out, lse, few)
+    again, lse2, _ = c.attend(d_q=d_q, ws=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2), "the same call differs"
+    assert q.spear_ec_workspace_status(ws) == 0
