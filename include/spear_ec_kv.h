@@ -157,7 +157,7 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  * held in fp32.  A probability and a value are rounded to fp16 on their way
  * (2^-11 relative each), whatever the scales of other tokens: a probability times
  * its value's scale is off by no more than 2^-11 of itself or, in calls of many
- * rows, 2^-27 of the row's largest such product, in calls of few 2^-38 of its
+ * rows, 2^-24 of the row's largest such product, in calls of few 2^-38 of its
  * largest probability times its largest scale, if that is more.  Whatever a row of
  * q holds, the others keep these bounds.
  * Scores past 2^23 (in powers of two), whose digits below 1 fp32 does not hold,

@@ -11,7 +11,7 @@
 // ahead and write them to LDS as fp16 matrix operands, so that the codes are
 // unpacked once per item and tile: keys as c - z, exact; values as
 // (c - z) s 2^-e with e the exponent of the block's largest scale, rounded
-// once (2^-11), or, where that scale is more than 16 times the block's smallest,
+// once (2^-11), or, where that scale is more than 128 times the block's smallest,
 // as c - z, whose scale the probability takes.  Two waves share a SIMD, w and
 // w + 4; the first stages the next tile before its own work on this one, so that
 // its matrix steps meet the other's vector work (staging by all eight waves, half
@@ -39,8 +39,9 @@
 // tokens, so, before scales and scores were held over their whole range: 789 and
 // 159 us).  In a block of scales far apart a token counts
 // with its own exponent and only for rows that see it, so that no row depends on
-// the scales of tokens without weight in it: fp16's smallest step is 2^-26 of the
-// row's largest product of probability and scale, below the error of O's fp32 sum.
+// the scales of tokens without weight in it: half of fp16's smallest step is at
+// most 2^-25 kAlike 2 2^-kBelow = 2^-24 of the row's largest product of probability
+// and scale, fp32's own rounding of that.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
 // steps and takes about 4500 (prompts of 4096 tokens 783-785 us, 870 TFLOP/s).
@@ -75,7 +76,11 @@ constexpr float kLarge = 0x1p23f;
 constexpr float kBelow = 7.f;        // M stands this far below the largest score plus e
 constexpr float kApart = 3e38f;      // an exponent that leaves no sum of weights below kMostSum
 constexpr float kMostSum = 65504.f;  // of a lane's eight weights, fp16's largest: above it M is raised
-constexpr float kAlike = 16.f;       // ratio of a block's value scales that takes them apart
+// Ratio of a block's value scales that takes them apart: with kBelow it bounds
+// what fp16's smallest step costs.  Prompts of 4096 tokens with normal logarithms
+// of the scales, of deviation 0.3 / 0.6 / 1 / 2: 792 / 954 / 1522 / 1563 us with a
+// ratio of 16, 792 / 791 / 891 / 1545 with 128.
+constexpr float kAlike = 128.f;
 
 // One tile as operands.  Rows are padded by 16 bytes, so that eight
 // consecutive lanes' 16-byte reads meet different banks and every offset is a

@@ -12,9 +12,10 @@ p_j = exp(S_j - m) / l, s_j the value's scale and v_j its codes less z:
   * a probability and a value are rounded to fp16, 2^-11 of themselves each:
     2^-10 + 2^-22 together;
   * O's sum, in fp32, runs over products with codes and zero-points up to 15
-    apart: (n / 16 + 64) u 30 sum p_j s_j.  In calls of many rows a p_j s_j is
-    also no finer than 2^-27 of the row's largest, which n times 15 of that, at
-    most n / 8 * 15 u, stays below;
+    apart: (n / 16 + 64) u 30 sum p_j s_j;
+  * in calls of many rows a p_j s_j is no finer than u times the row's largest:
+    weights start at 2^7 and lose at most half of fp16's smallest step, 2^-25,
+    for values of up to 2^8 times their token's scale: 2^-25 2^8 / 2^7;
   * in calls of few rows a p_j s_j is no finer than 2^-38 of the row's largest
     p_j times its largest s_j;
   * the output is rounded once to bf16.
@@ -66,9 +67,8 @@ def expected(c, few, scale=None, window=0):
             dp = np.where(top - second - 2 * dS > 100, 0.0, 2 * dS)[:, None]
             t = ((dp + 2.0 ** -10 + 2.0 ** -22 + 2.0 ** -18) * (pv @ np.abs(vc))
                  + ((seen.sum(1) / 16 + 64) * ref.U * 30 * pv.sum(1))[:, None])
-            if few:
-                t += ((2.0 ** -38 * p.max(1) * np.where(seen, vs, 0).max(1))[:, None]
-                      * (seen.astype(float) @ np.abs(vc)))
+            floor = 2.0 ** -38 * p.max(1) * np.where(seen, vs, 0).max(1) if few else ref.U * pv.max(1)
+            t += floor[:, None] * (seen.astype(float) @ np.abs(vc))
             t += ref.half_step_bf16(np.abs(o) + t)
             shape = (len(real), R)
             out[rows], tol[rows] = o.reshape(*shape, D), t.reshape(*shape, D)
