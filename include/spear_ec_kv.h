@@ -154,7 +154,8 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  *   lse  fp32 [tokens][q_heads], or NULL
  * Keys meet q exactly, but for elements below 2^-19 of their row's largest in
  * calls of many rows, which are off by at most 2^-27 of it; products and sums are
- * held in fp32.  A probability and a value are rounded to fp16 on their way
+ * held in fp32 (those of a value's codes and of its zero-point apart in calls of
+ * few rows).  A probability and a value are rounded to fp16 on their way
  * (2^-11 relative each), whatever the scales of other tokens: a probability times
  * its value's scale is off by no more than 2^-11 of itself or, in calls of many
  * rows, 2^-24 of the row's largest such product, in calls of few 2^-38 of its
@@ -163,6 +164,9 @@ size_t spear_ec_kv_workspace_bytes(const spear_ec_kv_desc* desc, int32_t n_seqs,
  * Scores past 2^23 (in powers of two), whose digits below 1 fp32 does not hold,
  * decide by the digits that it does; a row whose scores leave fp32 itself may hold
  * anything.
+ * A call of few rows is one with tokens * (q_heads / kv_heads) / n_seqs at most 64,
+ * or 128 in small calls.  That is an average, which single tokens and a long chunk
+ * in one call fit badly: two calls are faster there.
  * A padding row attends to nothing: zeros, lse = -inf.  softmax_scale is
  * positive and at most 2^64.  A q row holding an infinity or NaN gives NaN in that
  * row alone.  Bad pages: see SPEAR_EC_WS_BAD_PAGE.

@@ -30,7 +30,7 @@ namespace {
 // Rows a sequence has on average from which a call goes by blocks of
 // positions instead of rows.  By rows / by blocks, 64 and 8 heads of 128: 64
 // sequences of 4 rows 6.3 / 7.4 us, of 12 10.9 / 11.2, of 16 13.4 / 12.3, of 32
-// 21 / 18; one of 8 to 64 rows the same within 4%.
+// 21 / 18; one of 8 to 64 rows the same within 4%.  All of them even calls.
 constexpr int kChunkRows = 16;
 
 // Joins over the LANES (8 or 16) lanes of a vector by lane exchanges within

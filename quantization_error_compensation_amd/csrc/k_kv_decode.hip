@@ -46,7 +46,7 @@ constexpr int kGroups = 256;     // workgroups: one per compute unit of gfx950
 constexpr int kXcds = 8;         // consecutive workgroups go to them in turn
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kLarge = 0x1p23f;
+constexpr float kLarge = 0x1p23f;  // scores past it count times a power of two below it
 
 template <int D>
 constexpr int slot_floats() { return kRows * D + 2 * kRows; }

@@ -21,7 +21,8 @@
 // the rows to waves 4-7: such calls read the cache more often per row, and
 // waited for it (8 chats of 72 rows behind 4096 tokens: two workgroups of four
 // waves a compute unit 45 us, this one 42, with the cut by the items that there
-// are and all waves joining 35).
+// are and all waves joining 35, with scales and queries held over their whole
+// range 36).
 //
 // Scores.  S^T = K q^T (32x32x16): a lane holds one row and, with key row
 // bits 2 and 3 exchanged when the tile is written, runs of 8 consecutive
@@ -44,10 +45,11 @@
 // and scale, fp32's own rounding of that.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
-// steps and takes about 4500 (prompts of 4096 tokens 783-785 us, 870 TFLOP/s).
-// Counters there: matrix cores busy 38% of the time, vector units 50%, LDS 34%:
-// two waves a SIMD, all that 230 registers leave room for, wait for each other's
-// results rather than for one unit (32 fewer vector instructions a tile in the
+// steps and takes about 4500 (prompts of 4096 tokens 782-793 us, 870 TFLOP/s).
+// Counters there: matrix cores busy 37% of the time, vector units 50%, LDS 34%:
+// two waves a SIMD wait for each other's results rather than for one unit; more
+// do not fit, since items of 256 rows with heads of 128 take all 256 registers
+// (10 or 11 more live in scratch memory, in the join alone) (32 fewer vector instructions a tile in the
 // staging waves gained 0.5%).  Computing a tile's scores beside the previous
 // tile's softmax in one wave, with eight or four waves a workgroup, took 1.09 to
 // 1.2 times as long; staging by all waves and wave priorities gained nothing.
@@ -71,8 +73,8 @@ constexpr int kTileTarget = 256;
 constexpr int kTileMaxSplits = 32;
 constexpr int kMinTiles = 4;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr float kNever = -3e38f;  // M before any score: below any, and finite
-constexpr float kLarge = 0x1p23f;
+constexpr float kNever = -3e38f;     // M before any score: below any, and finite
+constexpr float kLarge = 0x1p23f;    // scores past it count times a power of two below it
 constexpr float kBelow = 7.f;        // M stands this far below the largest score plus e
 constexpr float kApart = 3e38f;      // an exponent that leaves no sum of weights below kMostSum
 constexpr float kMostSum = 65504.f;  // of a lane's eight weights, fp16's largest: above it M is raised
@@ -771,9 +773,9 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
 // average, or where that leaves fewer items than half the compute units, so that
 // 256 rows an item would leave long runs or a large join; 256 at a time
 // elsewhere.  Calls of 64 heads of 128 behind 4096 tokens, 128 rows / 256 rows:
-// one chat of 64 tokens 30 / 50 us, of 128 36 / 46, of 256 56 / 57, of 1024
-// 168 / 139; 32 chats of 16 tokens 98 / 123, of 32 197 / 157; 8 chats of 17
-// 55 / 47.
+// one chat of 64 tokens 31 / 50 us, of 128 39 / 46, of 256 59 / 58, of 1024
+// 172 / 146; 32 chats of 16 tokens 101 / 130, of 32 199 / 165; 8 chats of 17
+// 56 / 51.
 bool narrow(const KvShape& s, int n_seqs, int tokens) {
   const int64_t rows = ((int64_t)tokens * s.group() + n_seqs - 1) / n_seqs;
   return rows <= 128 || (rows + 127) / 128 * n_seqs * s.kv_heads < kTileTarget / 2;

@@ -98,11 +98,14 @@ KvCache make_kv_cache(const KvShape& s, const uint8_t* codes, const void* scales
 // Which calls take the kernel for many rows.  The one for few rows reads and
 // unpacks a cached token again for every 16 rows (token, query head of one kv
 // head) of its sequence, the one for many for every 128 or 256, but it starts
-// and joins slower: it pays from 64 rows a sequence on, or from 128 where 16 at
-// a time make no more items than there are compute units.  Few / many rows'
-// kernel, heads of 128 behind 4096 tokens: 8 chats of 64 rows 25 / 33 us, of 72
-// 37 / 35, of 128 47 / 38; 32 chats of 48 78 / 89, of 64 101 / 89; one chat of
-// 128 13 / 27; one of 72 behind 65536 57 / 68, of 128 78 / 75, of 192 118 / 103.
+// and joins slower: it pays past 64 rows a sequence, or past 128 where 16 at a
+// time make no more items than there are compute units.  Few / many rows'
+// kernel, heads of 128 behind 4096 tokens: 8 chats of 64 rows 25 / 35 us, of 72
+// 36 / 36, of 128 45 / 39; 9 chats of 64 33 / 61, 16 of 64 47 / 55, 32 of 48
+// 78 / 92, 32 of 64 101 / 93; one chat of 128 13 / 27; one of 72 behind 65536
+// 57 / 69, of 128 76 / 77, of 192 114 / 106; 40 of 64, heads of 64 behind 1024,
+// 37 / 47.  The lengths of the rows are device data: the rule goes by their
+// average, and these calls are even.
 constexpr int kFewRows = 64, kFewItems = 256;
 
 bool many_rows(const KvShape& s, int n_seqs, int tokens) {
