@@ -45,7 +45,7 @@
 // and scale, fp32's own rounding of that.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
-// steps and takes about 4500 (prompts of 4096 tokens 782-793 us, 870 TFLOP/s).
+// steps and takes about 4500 (prompts of 4096 tokens 782-807 us, 843-870 TFLOP/s).
 // Counters there: matrix cores busy 37% of the time, vector units 50%, LDS 34%:
 // two waves a SIMD wait for each other's results rather than for one unit; more
 // do not fit, since items of 256 rows with heads of 128 take all 256 registers
