@@ -38,21 +38,22 @@
 // are taken at once, and again, against a new M, where the sum says so (a
 // maximum per tile: 801 and 164 us for prompts of 4096 and a chunk of 512
 // tokens, so, before scales and scores were held over their whole range: 789 and
-// 159 us).  In a block of scales far apart a token counts
-// with its own exponent and only for rows that see it, so that no row depends on
-// the scales of tokens without weight in it: half of fp16's smallest step is at
-// most 2^-25 kAlike 2 2^-kBelow = 2^-24 of the row's largest product of probability
-// and scale, fp32's own rounding of that.
+// 159 us).  In a block of scales far apart a token counts with its own exponent
+// and only for rows that see it, so that no row depends on the scales of tokens
+// without weight in it: half of fp16's smallest step is at most
+// 2^-25 kAlike 2 2^-kBelow = 2^-24 of the row's largest product of probability and
+// scale, fp32's own rounding of that.
 //
 // Bound.  A tile of 64 tokens against 64 rows a SIMD is 2048 cycles of matrix
 // steps and takes about 4500 (prompts of 4096 tokens 782-807 us, 843-870 TFLOP/s).
 // Counters there: matrix cores busy 37% of the time, vector units 50%, LDS 34%:
-// two waves a SIMD wait for each other's results rather than for one unit; more
-// do not fit, since items of 256 rows with heads of 128 take all 256 registers
-// (10 or 11 more live in scratch memory, in the join alone) (32 fewer vector instructions a tile in the
-// staging waves gained 0.5%).  Computing a tile's scores beside the previous
-// tile's softmax in one wave, with eight or four waves a workgroup, took 1.09 to
-// 1.2 times as long; staging by all waves and wave priorities gained nothing.
+// two waves a SIMD wait for each other's results rather than for one unit (32
+// fewer vector instructions a tile in the staging waves gained 0.5%); more do not
+// fit, since items of 256 rows with heads of 128 take all 256 registers (10 or 11
+// more live in scratch memory, in the join alone).  Computing a tile's scores
+// beside the previous tile's softmax in one wave, with eight or four waves a
+// workgroup, took 1.09 to 1.2 times as long; staging by all waves and wave
+// priorities gained nothing.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
