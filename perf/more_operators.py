@@ -1,0 +1,289 @@
+"""Workloads of the 8-bit path: matrix products of int8 activations and weights
+with a scale for each token and each output channel, plain and gated, and what
+makes their operands: the root-mean-square norm with the residual's addition,
+and the quantization of rows.
+
+A vector of int8 codes c with one fp32 scale s stands for c * s.  Quantizing
+one (a token's activations, an output channel's weights):
+
+  s = the fp32 nearest to max|v| / 127 (1 where that is 0)
+  c = clamp(round(v / s), -127, 127), ties to even
+
+The four operators, for tokens t, inputs k and outputs n:
+
+  quantize  rows of bf16 or fp32 values to codes and scales
+  norm      h = bf16(x + r), u = h * w / sqrt(mean(h^2) + eps), quantized from
+            the unrounded u, or rounded to bf16 for a layer that reads bf16
+  linear    y[t, n] = sx[t] * sw[n] * sum_k cx[t, k] * cw[n, k]
+  gated     act(a) * b, a and b being linear's outputs for weight rows n and
+            n + d_out, act(a) = a * sigmoid(a) or the tanh form of GELU
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-5
+
+
+# ------------------------------------------------------------------- cases
+def _rows(name, op, tokens, width, **more):
+    return _named(name, dict(op=op, tokens=tokens, width=width, **more))
+
+
+def _product(name, op, tokens, d_in, d_out, act="none"):
+    return _named(name, dict(op=op, tokens=tokens, d_in=d_in, d_out=d_out, act=act))
+
+
+def _named(name, case):
+    return {**case, "name": name} if name else case
+
+
+def listed():
+    return [
+        # one chat's next token before a 4096-wide layer: all latency
+        _rows("norm_one", "norm", 1, 4096, residual=True, out="codes"),
+        # whole prompts before an 8192-wide layer
+        _rows("norm_prompts", "norm", 4096, 8192, residual=True, out="codes"),
+        # a ragged prompt's first norm, before a 4-bit layer: bf16, nothing to add
+        _rows("norm_bf16", "norm", 1333, 4096, residual=False, out="bf16"),
+        # 64 chats' gated activations before the projection back
+        _rows("quantize_batch", "quantize", 64, 28672, type="bf16"),
+        # a 4096 -> 11008 layer's weights when a model is loaded
+        _rows("quantize_weights", "quantize", 11008, 4096, type="fp32"),
+        # one chat's next token through an attention projection: weights once
+        _product("linear_one", "linear", 1, 4096, 4096),
+        # a decode step of 48 chats: queries, keys and values of 64 + 8 + 8 heads of 128
+        _product("linear_batch", "linear", 48, 8192, 10240),
+        # a 512-token chunk of a prompt through the projection back
+        _product("linear_chunk", "linear", 512, 28672, 8192),
+        # prompts through an attention projection
+        _product("linear_prompts", "linear", 4096, 8192, 8192),
+        # one chat's next token through both projections of a feed-forward block
+        _product("gated_one", "gated", 1, 4096, 11008, "silu"),
+        # verify pass of 8 chats, 9 tokens each (draft length + 1)
+        _product("gated_verify", "gated", 72, 8192, 28672, "silu"),
+        # prompts of an odd length: the largest product
+        _product("gated_prompts", "gated", 3999, 8192, 28672, "gelu"),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return int(round(lo * (hi / lo) ** rng.random()))
+
+
+def _width(rng, lo, hi):
+    """Multiples of 16, half of them of the usual 128."""
+    step = 128 if rng.random() < 0.5 else 16
+    return max(step, _spread(rng, lo, hi) // step * step)
+
+
+def draw(rng):
+    op = rng.choice(["norm", "quantize", "linear", "linear", "gated"])
+    if op in ("norm", "quantize"):
+        width = _width(rng, 128, 28672)
+        tokens = _spread(rng, 1, 4096 * 8192 // width)
+        if op == "quantize":
+            return _rows("", op, tokens, width, type=rng.choice(["bf16", "bf16", "fp32"]))
+        return _rows("", op, tokens, width, residual=rng.random() < 0.7,
+                     out=rng.choice(["codes", "codes", "bf16"]))
+    d_in, d_out = _width(rng, 256, 28672), _width(rng, 256, 28672)
+    kind = rng.choice(["one", "decode", "verify", "prompts"])
+    tokens = {"one": 1, "decode": _spread(rng, 2, 64), "verify": _spread(rng, 65, 256),
+              "prompts": _spread(rng, 257, 4096)}[kind]
+    most = 3999 * 8192 * 28672  # the largest listed case's products (of one projection)
+    if tokens * d_in * d_out > most:
+        tokens = most // (d_in * d_out)
+    return _product("", op, tokens, d_in, d_out,
+                    rng.choice(["silu", "silu", "gelu"]) if op == "gated" else "none")
+
+
+def work(case):
+    T = case["tokens"]
+    if case["op"] in ("norm", "quantize"):
+        d, n = case["width"], T * case["width"]
+        if case["op"] == "quantize":  # and the codes read back as values
+            return {"bytes": n * ((4 if case["type"] == "fp32" else 2) + 1 + 1 + 4) + 8 * T,
+                    "flops": 4 * n}
+        out = n * 2 if case["out"] == "bf16" else n * (1 + 1 + 4) + 8 * T
+        return {"bytes": n * (2 + (4 if case["residual"] else 0)) + 2 * d + out, "flops": 8 * n}
+    K, N = case["d_in"], case["d_out"]
+    rows = N * (2 if case["op"] == "gated" else 1)
+    return {"bytes": rows * (K + 4) + T * (K + 4) + 2 * T * N, "flops": 2 * T * K * rows}
+
+
+# ------------------------------------------------------------------ inputs
+def _activations(g, tokens, width):
+    """Normal values with one channel in a hundred 20 times as large, as a
+    model's hidden states have them."""
+    x = torch.randn((tokens, width), generator=g, device="cuda")
+    big = torch.randint(0, width, (-(-width // 100),), generator=g, device="cuda")
+    x[:, big] *= 20.0
+    return x
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(int(seed))
+    T = case["tokens"]
+    s = dict(case=case)
+    if own:
+        import quantization_error_compensation_amd as lib
+        s["lib"] = lib
+    if case["op"] in ("norm", "quantize"):
+        d = case["width"]
+        x = _activations(g, T, d)
+        s["x"] = x if case.get("type") == "fp32" else x.bfloat16()
+        if case["op"] == "norm":
+            s["residual"] = s["sum"] = s["y"] = None
+            if case["residual"]:
+                s["residual"] = _activations(g, T, d).bfloat16()
+                s["sum"] = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+            s["weight"] = (1 + 0.1 * torch.randn(d, generator=g, device="cuda")).bfloat16()
+            if case["out"] == "bf16":
+                s["y"] = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+        s["codes"] = s["scales"] = None
+        if case.get("out") != "bf16":
+            s["codes"] = torch.empty((T, d), dtype=torch.int8, device="cuda")
+            s["scales"] = torch.empty(T, dtype=torch.float32, device="cuda")
+            s["values"] = torch.empty((T, d), dtype=torch.float32, device="cuda")
+        return s
+    K, N = case["d_in"], case["d_out"]
+    rows = 2 * N if case["op"] == "gated" else N
+    x = _activations(g, T, K)
+    s["sx"] = x.abs().amax(1) / 127
+    s["cx"] = (x / s["sx"][:, None]).round_().clamp_(-127, 127).to(torch.int8)
+    # what quantizing normal weights of deviation 1 / sqrt(d_in) leaves: codes of
+    # about 30 steps' spread
+    s["cw"] = torch.empty((rows, K), dtype=torch.int8, device="cuda")
+    step = max(1, (1 << 26) // K)
+    for i in range(0, rows, step):
+        w = torch.randn((min(step, rows - i), K), generator=g, device="cuda")
+        s["cw"][i:i + step] = w.mul_(30).round_().clamp_(-127, 127).to(torch.int8)
+    s["sw"] = torch.exp(0.1 * torch.randn(rows, generator=g, device="cuda")) / (30 * math.sqrt(K))
+    s["y"] = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    if own:  # the handles that a program makes once
+        s["desc"] = s["lib"].make_q8_desc(K, N, case["act"])
+        s["workspace"] = s["lib"].alloc_q8_workspace(s["desc"], T)
+    return s
+
+
+# --------------------------------------------------------------- one pass
+def run(s):
+    return _run_own(s) if own else _run_plain(s)
+
+
+def _run_own(s):
+    lib, case = s["lib"], s["case"]
+    if case["op"] in ("linear", "gated"):
+        lib.spear_ec_q8_linear(s["desc"], s["cx"], s["sx"], s["cw"], s["sw"], s["y"], s["workspace"])
+        return s["y"]
+    first = ()
+    if case["op"] == "quantize":
+        lib.spear_ec_q8_quantize(s["x"], s["codes"], s["scales"])
+    else:
+        lib.spear_ec_q8_rmsnorm(s["x"], s["residual"], s["sum"], s["weight"], EPS, y=s["y"],
+                                codes=s["codes"], scales=s["scales"])
+        first = tuple(t for t in (s["sum"], s["y"]) if t is not None)
+    if s["codes"] is None:
+        return first
+    lib.spear_ec_q8_dequant_f32(s["codes"], s["scales"], s["values"])
+    return (*first, s["values"])
+
+
+def _run_plain(s):
+    op = s["case"]["op"]
+    if op in ("linear", "gated"):
+        return _plain_product(s)
+    return _plain_quantize(s) if op == "quantize" else _plain_norm(s)
+
+
+def _plain_codes(s, v):
+    """Codes and scales of the rows of a 64-bit v (where a value falls next to a border
+    between two codes, 32 bits would choose another one), and what they stand for."""
+    scale = (v.abs().amax(1) / 127).float()
+    scale = torch.where(scale == 0, torch.ones_like(scale), scale)
+    s["scales"].copy_(scale)
+    s["codes"].copy_((v / scale.double()[:, None]).round_().clamp_(-127, 127))
+    torch.mul(s["codes"].float(), scale[:, None], out=s["values"])
+    return s["values"]
+
+
+def _plain_quantize(s):
+    return _plain_codes(s, s["x"].double())
+
+
+def _plain_norm(s):
+    h, first = s["x"], ()
+    if s["residual"] is not None:
+        s["sum"].copy_(s["x"].float() + s["residual"].float())
+        h, first = s["sum"], (s["sum"],)
+    h = h.double()
+    u = h * ((h * h).mean(1, keepdim=True) + EPS).rsqrt() * s["weight"].double()
+    if s["y"] is not None:
+        s["y"].copy_(u)
+        first = (*first, s["y"])
+    return first if s["codes"] is None else (*first, _plain_codes(s, u))
+
+
+def _plain_product(s):
+    case, N = s["case"], s["case"]["d_out"]
+    y = torch.matmul(s["cx"].float(), s["cw"].float().t())
+    y.mul_(s["sx"][:, None]).mul_(s["sw"])
+    if case["op"] == "gated":
+        a, b = y[:, :N], y[:, N:]
+        z = a
+        if case["act"] == "gelu":
+            z = 2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a * a * a)
+        y = a / (1 + torch.exp(-z)) * b
+    s["y"].copy_(y)
+    return s["y"]
+
+
+# ------------------------------------------------- the definition, in 64 bits
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] in ("linear", "gated"):
+        return _exact_product(case, s)
+    if case["op"] == "quantize":
+        return _exact_values(s["x"].to(torch.float64))
+    out = []
+    h = s["x"].to(torch.float64)
+    if case["residual"]:
+        h = (h + s["residual"].to(torch.float64)).to(torch.bfloat16).to(torch.float64)
+        out.append(h)
+    length = torch.linalg.vector_norm(h, dim=1, keepdim=True)
+    u = s["weight"].to(torch.float64) * h / torch.sqrt(length ** 2 / case["width"] + EPS)
+    out.append(u if case["out"] == "bf16" else _exact_values(u))
+    return tuple(out)
+
+
+def _exact_values(v):
+    largest = torch.maximum(v.max(dim=1).values, -v.min(dim=1).values)
+    scale = torch.div(largest, 127).to(torch.float32).to(torch.float64)
+    scale[scale == 0] = 1
+    q = torch.round(torch.div(v, scale.unsqueeze(1)))
+    return torch.clip(q, min=-127, max=127) * scale.unsqueeze(1)
+
+
+def _exact_product(case, s):
+    T, N = case["tokens"], case["d_out"]
+    x = s["cx"].to(torch.float64) * s["sx"].to(torch.float64).unsqueeze(1)
+    out = torch.empty((T, N), dtype=torch.float64, device="cuda")
+
+    def rows(i, n):
+        return x @ (s["cw"][i:i + n].to(torch.float64) * s["sw"][i:i + n, None].to(torch.float64)
+                    ).transpose(0, 1)
+
+    for i in range(0, N, 4096):
+        n = min(4096, N - i)
+        if case["op"] == "linear":
+            out[:, i:i + n] = rows(i, n)
+            continue
+        a = rows(i, n)
+        if case["act"] == "silu":
+            a = a * torch.sigmoid(a)
+        else:
+            a = 0.5 * a * (1 + torch.tanh(math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)))
+        out[:, i:i + n] = a * rows(N + i, n)
+    return out
