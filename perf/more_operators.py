@@ -174,12 +174,12 @@ def run(s):
 
 
 def _run_own(s):
-    lib, case = s["lib"], s["case"]
-    if case["op"] in ("linear", "gated"):
+    lib, op = s["lib"], s["case"]["op"]
+    if op in ("linear", "gated"):
         lib.spear_ec_q8_linear(s["desc"], s["cx"], s["sx"], s["cw"], s["sw"], s["y"], s["workspace"])
         return s["y"]
     first = ()
-    if case["op"] == "quantize":
+    if op == "quantize":
         lib.spear_ec_q8_quantize(s["x"], s["codes"], s["scales"])
     else:
         lib.spear_ec_q8_rmsnorm(s["x"], s["residual"], s["sum"], s["weight"], EPS, y=s["y"],
@@ -188,7 +188,7 @@ def _run_own(s):
     if s["codes"] is None:
         return first
     lib.spear_ec_q8_dequant_f32(s["codes"], s["scales"], s["values"])
-    return (*first, s["values"])
+    return (*first, s["values"]) if op == "norm" else s["values"]
 
 
 def _run_plain(s):
