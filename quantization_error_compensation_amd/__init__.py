@@ -2,11 +2,12 @@
 
 y = dequant(Wq) x + alpha * B diag(gamma(A x)) A x with gamma(u) =
 sigmoid(g * u + b) (SPEAR summary, section 2.1 A), computed by hand-written
-HIP kernels behind the C ABI declared in include/spear_ec.h, and the 4-bit
-paged key/value cache of include/spear_ec_kv.h: appending, attention and
-reading back.  This package holds the kernels (csrc/), their build script
-(build.py) and a ctypes binding (binding.py, kv.py) with the same names as the
-C entry points.  PyTorch is used only
+HIP kernels behind the C ABI declared in include/spear_ec.h; the 4-bit paged
+key/value cache of include/spear_ec_kv.h: appending, attention and reading
+back; and the 8-bit path of include/spear_ec_q8.h: norm and quantization of
+rows, int8 matrix products plain and gated.  This package holds the kernels
+(csrc/), their build script (build.py) and a ctypes binding (binding.py, kv.py,
+q8.py) with the same names as the C entry points.  PyTorch is used only
 to hold device memory and to supply the current stream.
 """
 from .binding import (  # noqa: F401
@@ -26,6 +27,11 @@ from .kv import (  # noqa: F401
     KV_EXPORTED, SPEAR_EC_WS_BAD_PAGE, alloc_kv_cache, alloc_kv_workspace, kv_cache_shapes,
     make_kv_batch, make_kv_desc, spear_ec_kv_append, spear_ec_kv_attention, spear_ec_kv_batch,
     spear_ec_kv_dequant_f32, spear_ec_kv_desc, spear_ec_kv_rope, spear_ec_kv_workspace_bytes,
+)
+from .q8 import (  # noqa: F401
+    Q8_EXPORTED, SPEAR_EC_Q8_GATED, SPEAR_EC_Q8_GELU, alloc_q8, alloc_q8_workspace, make_q8_desc,
+    q8_weight_shape, spear_ec_q8_dequant_f32, spear_ec_q8_desc, spear_ec_q8_linear,
+    spear_ec_q8_quantize, spear_ec_q8_rmsnorm, spear_ec_q8_workspace_bytes,
 )
 
 
