@@ -98,7 +98,8 @@ int spear_ec_q8_rmsnorm(int32_t rows, int32_t width, const void* x, int64_t x_st
 size_t spear_ec_q8_workspace_bytes(const spear_ec_q8_desc* desc, int32_t max_tokens);
 
 /*
- * Matrix product, 0 .. 2^20 tokens (0: nothing is launched):
+ * Matrix product, 0 .. 2^20 tokens (0: nothing is launched), tokens * d_out at
+ * most 2^37:
  *   p[t][n] = xs[t] * ws[n] * sum_k xq[t][k] * wq[n][k]
  *   y[t][n] = p[t][n], or with SPEAR_EC_Q8_GATED act(p[t][n]) * p[t][n + d_out]
  *   act(a)  = a * sigmoid(a), or with SPEAR_EC_Q8_GELU

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libspear_ec.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "static_scratch.hip", "k_quant.hip", "k_proj.hip", "k_decode.hip",
            "k_prefill.hip", "scheduler.cpp", "kv_api.hip", "k_kv_append.hip", "k_kv_decode.hip",
-           "k_kv_prefill.hip", "q8_api.hip", "k_q8_rows.hip", "k_q8_gemm.hip"]
+           "k_kv_prefill.hip", "q8_api.hip", "k_q8_rows.hip", "k_q8_gemm.hip",
+           "k_q8_stream.hip"]
 ARCH = os.environ.get("SPEAR_EC_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

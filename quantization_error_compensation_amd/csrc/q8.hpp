@@ -41,6 +41,8 @@ hipError_t launch_q8_quantize(int rows, int width, const void* x, bool x_f32, in
 hipError_t launch_q8_dequant(int rows, int width, const int8_t* codes, const float* scales,
                              float* out, hipStream_t st);
 hipError_t launch_q8_norm(int rows, int width, const Q8Norm& a, hipStream_t st);
+struct Q8Stream;  // q8_plan.hpp
+hipError_t launch_q8_stream(const Q8Shape& s, const Q8Product& a, const Q8Stream& f, hipStream_t st);
 // Bytes of workspace of calls of up to s.T tokens, and launch of the product.
 size_t q8_product_workspace(const Q8Shape& s);
 hipError_t launch_q8_product(const Q8Shape& s, const Q8Product& a, void* workspace, hipStream_t st);

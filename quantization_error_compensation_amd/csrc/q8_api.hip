@@ -138,7 +138,8 @@ int spear_ec_q8_linear(const spear_ec_q8_desc* desc, int32_t tokens, const int8_
   int rc = check_q8_desc(desc);
   if (rc) return rc;
   if (tokens < 0) return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "tokens is negative");
-  if (tokens > kQ8MaxTokens) return fail(SPEAR_EC_ERR_UNSUPPORTED, "at most 2^20 tokens");
+  if (tokens > kQ8MaxTokens || (int64_t)tokens * desc->d_out > (int64_t)1 << 37)
+    return fail(SPEAR_EC_ERR_UNSUPPORTED, "at most 2^20 tokens, tokens * d_out at most 2^37");
   if (tokens == 0) return SPEAR_EC_OK;
   rc = check_codes(xq, xs);
   if (!rc) rc = check_codes(wq, ws);

@@ -1,0 +1,136 @@
+// Which kernel a product of the 8-bit path takes, and the workspace it needs
+// (host code).
+//
+// Up to 16 tokens, and up to 32 or 64 where that still pays, the weights are
+// streamed by workgroups that hold 16 to 64 of their rows over the whole of K
+// (k_q8_stream.hip); past that a workgroup multiplies a tile of tokens with a
+// tile of rows (k_q8_gemm.hip).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "q8.hpp"
+
+namespace spear {
+
+constexpr int kQ8Units = 256;            // compute units of gfx950
+constexpr int kQ8CounterBytes = 16384;   // arrival counters at the head of the workspace
+constexpr int kQ8MaxSplitTiles = 1024;   // of them tiles' arrivals
+constexpr int64_t kQ8MaxPartials = (int64_t)64 << 20;
+constexpr int kQ8MaxSplits = 8;
+
+// ------------------------------------------------------------- few tokens
+// x: loads of 8 tokens a block of K (1, 2, 4, 6, 8); tiles: 16-row tiles of the
+// weights (of each projection) a workgroup; waves.
+struct Q8Stream {
+  int x, tiles, waves;  // x 0: the tile kernel
+};
+
+// The rows that the fullest compute unit streams, and the tokens' codes that
+// come along with them, decide: a unit reads tiles * 2 KB of weights and x KB
+// of tokens a block and workgroup.  More rows a workgroup read the tokens less
+// often, fewer fill the units more evenly.  us for 1 / 2 / 4 tiles:
+//   16 tokens  4096x4096 4.7 / 4.9 / 6.0   4096->6144 6.1 / 5.8 / 6.2
+//              28672->8192 45.5 / 40.4 / 53.4   8192->10240 18.9 / 20.8 / 17.8
+//   32 tokens  28672->8192 57.6 / 45.8 / 60.9   8192->10240 23.7 / 25.3 / 19.9
+// Up to 8 tokens there is next to nothing to share: one tile (28672->8192 40.2,
+// two 40.4).  One tile with at most 256 workgroups and K >= 8192: 8 waves
+// instead of 4 (8192->1024, one token, 4.2 against 5.2; 11008->4096 10.1 against
+// 11.1; but 4096x4096 4.7 against 4.5).
+inline Q8Stream plan_q8_stream(const Q8Shape& s) {
+  const int n = s.N / 16, parts = s.gated ? 2 : 1;
+  // Past 32 tokens only layers that the tile kernel would have to split over K
+  // to fill the units, whose join costs more than the tokens' repeated reads: 64
+  // tokens, 4096x4096 6.3 against 9.0 us, 4096->6144 7.7 against 9.6, 8192->1024
+  // 8.4 against 9.6; 11008->4096 17.4 against 14.9, 8192x8192 19.8 against 17.7.
+  if (s.T > 64 || (s.T > 32 && (n > 384 || s.K > 8192))) return Q8Stream{0, 0, 0};
+  Q8Stream best{s.T <= 8 ? 1 : s.T <= 16 ? 2 : s.T <= 32 ? 4 : s.T <= 48 ? 6 : 8, 1, 4};
+  if (best.x > 1) {
+    int64_t least = INT64_MAX;
+    for (int tiles = 1; tiles <= (best.x <= 4 ? 4 : 2); tiles *= 2) {
+      const int groups = (n + tiles - 1) / tiles;
+      const int64_t cost = (int64_t)((groups + kQ8Units - 1) / kQ8Units) * (2 * tiles * parts + best.x);
+      if (cost < least) {
+        least = cost;
+        best.tiles = tiles;
+      }
+    }
+  }
+  if (best.x <= 2 && best.tiles == 1 && n <= kQ8Units && s.K >= 8192) best.waves = 8;
+  return best;
+}
+
+// ------------------------------------------------------------ many tokens
+// The tile kernel's shapes: tokens x weight rows, waves, LDS of a workgroup
+// decides how many of them a compute unit holds; block: us that a unit needs
+// for 128 codes of K of a tile, once: us that a tile's start and end add.
+// (Fitted to 1400 timings of 16 layers at 24 to 4096 tokens; the rule's choice
+// is 1.1% slower than the best of them on average.)
+struct Q8Tile {
+  int bm, bn, held;  // held: workgroups a unit
+  bool gated;        // a wave holds both projections of its columns
+  double block, once;
+};
+constexpr Q8Tile kQ8Tiles[] = {
+    {256, 256, 1, true, 1.33, 5.4}, {192, 256, 1, true, 1.15, 3.5}, {128, 256, 1, true, 0.75, 3.4},
+    {128, 128, 1, false, 0.45, 3.1}, {64, 128, 2, true, 0.29, 3.5}, {64, 64, 2, false, 0.175, 3.4},
+    {32, 128, 2, false, 0.21, 3.1}};
+constexpr int kQ8TileCount = sizeof(kQ8Tiles) / sizeof(kQ8Tiles[0]);
+
+struct Q8TilePlan {
+  int tile, splits;
+  int64_t tiles;
+};
+
+inline int64_t q8_tiles(const Q8Shape& s, const Q8Tile& t) {
+  const int cols = s.gated ? t.bn / 2 : t.bn;
+  return (int64_t)((s.T + t.bm - 1) / t.bm) * ((s.N + cols - 1) / cols);
+}
+
+// The shape and the number of splits of K with the least estimated time: the
+// fullest unit's tiles, the part of the memory traffic that does not hide behind
+// them (as if at 10 TB/s), and the partial sums' way through memory.  Splits
+// fill the units where tiles are few: 28672->8192 at 512 tokens, 256 x 128 tiles
+// of 128 x 256, 124 us with 2 splits (each unit half a tile's K), 128 x 128
+// without splits 144; 8192x8192 at 256 tokens 29.5 with 2 splits of 128 x 128,
+// 33.6 with 64 x 128 and none.
+inline Q8TilePlan plan_q8_tiles(const Q8Shape& s) {
+  Q8TilePlan best{0, 1, q8_tiles(s, kQ8Tiles[0])};
+  double least = 1e300;
+  const int blocks = (s.K + 127) / 128;
+  const double rows = s.gated ? 2.0 * s.N : s.N;
+  const double memory = (rows * s.K + (double)s.T * s.K + 2.0 * s.T * s.N) / 10e6;
+  for (int i = 0; i < kQ8TileCount; ++i) {
+    const Q8Tile& t = kQ8Tiles[i];
+    if (s.gated && !t.gated) continue;
+    const int64_t tiles = q8_tiles(s, t);
+    if (i > 0 && tiles > 1 << 22) continue;  // a launch holds fewer than 2^32 threads
+    for (int splits = 1; splits <= kQ8MaxSplits && splits <= blocks; ++splits) {
+      if (splits > 1 && (tiles > kQ8MaxSplitTiles || tiles * splits * t.bm * t.bn * 4 > kQ8MaxPartials ||
+                         (t.bm * t.bn > 128 * 256 && splits > 2)))
+        break;
+      const int64_t each = (tiles * splits + kQ8Units - 1) / kQ8Units;
+      double us = (double)each * ((blocks + splits - 1) / splits) * t.block + memory +
+                  (double)((each + t.held - 1) / t.held) * t.once;
+      if (splits > 1)
+        us += 0.2 + 0.6 * splits + (0.45 * (splits - 1) + 1.4) * (double)each * t.bm * t.bn / 16384;
+      if (us < least) {
+        least = us;
+        best = Q8TilePlan{i, splits, tiles};
+      }
+    }
+  }
+  return best;
+}
+
+// Bytes of workspace for calls of up to s.T tokens: the counters and room for
+// the partial sums of any of them (tiles round tokens and rows up to at most
+// 255 more).
+inline size_t q8_workspace_for(const Q8Shape& s) {
+  if (s.T <= 32) return kQ8CounterBytes;
+  const int64_t all = (int64_t)kQ8MaxSplits * (s.T + 256) * (s.rows() + 256) * 4;
+  return (size_t)(kQ8CounterBytes + (all < kQ8MaxPartials ? all : kQ8MaxPartials));
+}
+
+}  // namespace spear
