@@ -21,7 +21,7 @@
  * spear_ec.h and spear_ec_last_error(); matrices 16-byte aligned, vectors of
  * scales 4-byte aligned).  Rows are contiguous, one after the other, but where
  * a stride is given.  width and d_in are multiples of 16 up to 65536, so that
- * rows begin on 16 bytes.
+ * rows begin on 16 bytes; rows are at most 2^30.
  */
 #ifndef SPEAR_EC_Q8_H
 #define SPEAR_EC_Q8_H
@@ -110,7 +110,8 @@ size_t spear_ec_q8_workspace_bytes(const spear_ec_q8_desc* desc, int32_t max_tok
  * Sums are exact 32-bit integers, whatever way the work is split: a row of y
  * depends on its own token and weight rows alone, bit for bit.  p takes three
  * fp32 roundings (the sum's conversion, times xs, times ws); where the sum times
- * xs leaves fp32's normal range so may p.  act is computed in fp32, its sigmoid
+ * xs leaves fp32's normal range so may p.  A bf16 y below 2^-126 may be zero.
+ * act is computed in fp32, its sigmoid
  * within 2^-15 of itself where that is above 2^-126.
  */
 int spear_ec_q8_linear(const spear_ec_q8_desc* desc, int32_t tokens, const int8_t* xq,

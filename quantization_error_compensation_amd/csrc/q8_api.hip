@@ -12,8 +12,8 @@ bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0;
 int check_rows_width(int32_t rows, int32_t width) {
   if (rows < 0 || width <= 0)
     return fail(SPEAR_EC_ERR_INVALID_ARGUMENT, "rows is negative or width not positive");
-  if (width % 16 != 0 || width > kQ8MaxWidth)
-    return fail(SPEAR_EC_ERR_UNSUPPORTED, "width must be a multiple of 16 up to 65536");
+  if (width % 16 != 0 || width > kQ8MaxWidth || rows > 1 << 30)
+    return fail(SPEAR_EC_ERR_UNSUPPORTED, "width must be a multiple of 16 up to 65536, rows at most 2^30");
   return SPEAR_EC_OK;
 }
 

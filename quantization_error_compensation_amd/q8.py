@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import SPEAR_EC_OUT_F32, load_library
+from .binding import SPEAR_EC_OUT_F32, _check, load_library
 from .kv import _call
 
 SPEAR_EC_Q8_GATED = 8
@@ -25,12 +25,13 @@ class spear_ec_q8_desc(ctypes.Structure):
     _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
-_q8_lib = None
+_q8_lib = _int8 = _bf16 = _f32 = _stream_of = _device_now = None
 
 
 def _lib():
-    global _q8_lib
+    global _q8_lib, _int8, _bf16, _f32, _stream_of, _device_now
     if _q8_lib is None:
+        import torch
         lib = load_library()
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         DP = ctypes.POINTER(spear_ec_q8_desc)
@@ -42,6 +43,9 @@ def _lib():
         for name in Q8_EXPORTED:
             getattr(lib, name).restype = ctypes.c_int
         lib.spear_ec_q8_workspace_bytes.restype = sz
+        _int8, _bf16, _f32 = torch.int8, torch.bfloat16, torch.float32
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _device_now = getattr(torch._C, "_cuda_getDevice", None)
         _q8_lib = lib
     return _q8_lib
 
@@ -82,86 +86,105 @@ def spear_ec_q8_workspace_bytes(desc, max_tokens: int) -> int:
     return int(_lib().spear_ec_q8_workspace_bytes(ctypes.byref(desc), int(max_tokens)))
 
 
-def _matrix(t, dtype, shape, device, name):
-    """Pointer of a contiguous matrix."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)} on one device "
-                         "with the call's other tensors")
-    return t.data_ptr()
+# Single-token calls take a few microseconds on the GPU, so the checks below are
+# written out in one expression a call: a helper for each tensor costs a third
+# of a microsecond apiece.
+def _run(fn, dev, stream, *args):
+    """fn on the device, on the stream (by default the device's current one)."""
+    if stream is None and dev >= 0 and dev == _device_now():
+        status = fn(*args, _stream_of(dev))
+        if status:
+            _check(status)
+    else:
+        _call(fn, dev, stream, *args)
 
 
-def _rows(t, dtypes, name):
-    """Shape, row stride and device of a matrix whose rows may be strided."""
-    shape = t.shape
-    if t.dtype not in dtypes or len(shape) != 2:
-        raise ValueError(f"{name} must be a matrix of " + " or ".join(str(d) for d in dtypes))
-    row, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    return shape, row if shape[0] > 1 else shape[1], t.get_device()
-
-
-def _codes(codes, scales, shape, device, name):
-    import torch
-    return (_matrix(codes, torch.int8, shape, device, name),
-            _matrix(scales, torch.float32, shape[:1], device, name + "'s scales"))
+def _strided(x, shape, name):
+    """Row stride of a matrix whose rows may be strided."""
+    if len(shape) != 2 or (shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return x.stride(0) if shape[0] > 1 else shape[1]
 
 
 def spear_ec_q8_quantize(x, codes, scales, stream=None):
     """Quantize the rows of x (bf16 or fp32 [rows, width], rows may be strided)."""
-    import torch
-    shape, stride, dev = _rows(x, (torch.bfloat16, torch.float32), "x")
-    cp, sp = _codes(codes, scales, shape, dev, "codes")
-    _call(_lib().spear_ec_q8_quantize, dev, stream, shape[0], shape[1], x.data_ptr(),
-          x.dtype is torch.float32, stride, cp, sp)
+    lib = _q8_lib or _lib()
+    shape, dev, kind = x.shape, x.get_device(), x.dtype
+    stride = _strided(x, shape, "x")
+    if (kind is not _bf16 and kind is not _f32) or codes.dtype is not _int8 or scales.dtype is not _f32 or \
+            codes.shape != shape or scales.shape != shape[:1] or codes.get_device() != dev or \
+            scales.get_device() != dev or not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("x must be bf16 or fp32, codes contiguous int8 of x's shape and scales contiguous "
+                         "fp32 with an element a row, on one device")
+    _run(lib.spear_ec_q8_quantize, dev, stream, shape[0], shape[1], x.data_ptr(), kind is _f32, stride,
+         codes.data_ptr(), scales.data_ptr())
 
 
 def spear_ec_q8_dequant_f32(codes, scales, out, stream=None):
     """Quantized rows as fp32 values [rows, width]."""
-    import torch
+    lib = _q8_lib or _lib()
     shape, dev = codes.shape, codes.get_device()
-    if len(shape) != 2:
-        raise ValueError("codes must be a matrix")
-    cp, sp = _codes(codes, scales, shape, dev, "codes")
-    _call(_lib().spear_ec_q8_dequant_f32, dev, stream, shape[0], shape[1], cp, sp,
-          _matrix(out, torch.float32, shape, dev, "out"))
+    if len(shape) != 2 or codes.dtype is not _int8 or scales.dtype is not _f32 or out.dtype is not _f32 or \
+            scales.shape != shape[:1] or out.shape != shape or scales.get_device() != dev or \
+            out.get_device() != dev or not codes.is_contiguous() or not scales.is_contiguous() or \
+            not out.is_contiguous():
+        raise ValueError("codes must be a contiguous int8 matrix, scales fp32 with an element a row and out "
+                         "fp32 of codes' shape, contiguous on one device")
+    _run(lib.spear_ec_q8_dequant_f32, dev, stream, shape[0], shape[1], codes.data_ptr(), scales.data_ptr(),
+         out.data_ptr())
+
+
+def _rows_like(t, shape, dev, name):
+    """Pointer of a contiguous bf16 matrix, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not _bf16 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous bf16 of x's shape, on x's device")
+    return t.data_ptr()
 
 
 def spear_ec_q8_rmsnorm(x, residual, sum, weight, eps, y=None, codes=None, scales=None, stream=None):
     """Norm of the rows of x, or of x + residual, which goes to sum (both may
     be None); to y (bf16) and/or quantized to codes and scales."""
-    import torch
-    bf16 = torch.bfloat16
-    shape, stride, dev = _rows(x, (bf16,), "x")
-    wp = _matrix(weight, bf16, shape[1:], dev, "weight")
-    rp = _matrix(residual, bf16, shape, dev, "residual") if residual is not None else None
-    up = _matrix(sum, bf16, shape, dev, "sum") if sum is not None else None
-    yp = _matrix(y, bf16, shape, dev, "y") if y is not None else None
+    lib = _q8_lib or _lib()
+    shape, dev = x.shape, x.get_device()
+    stride = _strided(x, shape, "x")
+    if x.dtype is not _bf16 or weight.dtype is not _bf16 or weight.shape != shape[1:] or \
+            weight.get_device() != dev or not weight.is_contiguous():
+        raise ValueError("x must be bf16 and weight contiguous bf16 with an element a column, on one device")
     cp = sp = None
-    if codes is not None or scales is not None:
-        if codes is None or scales is None:
-            raise ValueError("codes and scales are given together or not at all")
-        cp, sp = _codes(codes, scales, shape, dev, "codes")
-    _call(_lib().spear_ec_q8_rmsnorm, dev, stream, shape[0], shape[1], x.data_ptr(), stride, rp, up,
-          wp, eps, yp, cp, sp)
+    if codes is not None and scales is not None:
+        if codes.dtype is not _int8 or scales.dtype is not _f32 or codes.shape != shape or \
+                scales.shape != shape[:1] or codes.get_device() != dev or scales.get_device() != dev or \
+                not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes must be contiguous int8 of x's shape and scales contiguous fp32 with an "
+                             "element a row, on x's device")
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales are given together or not at all")
+    _run(lib.spear_ec_q8_rmsnorm, dev, stream, shape[0], shape[1], x.data_ptr(), stride,
+         _rows_like(residual, shape, dev, "residual"), _rows_like(sum, shape, dev, "sum"), weight.data_ptr(), eps,
+         _rows_like(y, shape, dev, "y"), cp, sp)
 
 
 def spear_ec_q8_linear(desc, xq, xs, wq, ws, y, workspace, stream=None):
     """y = act-gated or plain product of quantized rows: xq int8 [tokens, d_in]
     with scales xs, wq int8 of q8_weight_shape(desc) with scales ws, y bf16 (or
     fp32) [tokens, d_out]."""
-    import torch
-    shape, dev = xq.shape, xq.get_device()
-    if len(shape) != 2 or shape[1] != desc.d_in:
-        raise ValueError("xq must be a matrix of d_in columns")
-    flags = desc.flags
-    xp, xsp = _codes(xq, xs, shape, dev, "xq")
-    wp, wsp = _codes(wq, ws, torch.Size((desc.d_out * (2 if flags & SPEAR_EC_Q8_GATED else 1),
-                                         desc.d_in)), dev, "wq")
-    yp = _matrix(y, torch.float32 if flags & SPEAR_EC_OUT_F32 else torch.bfloat16,
-                 torch.Size((shape[0], desc.d_out)), dev, "y")
-    ok = workspace is not None and workspace.get_device() == dev and workspace.is_contiguous()
-    if not ok:
-        raise ValueError("the workspace must be contiguous, on one device with the call's tensors")
-    _call(_lib().spear_ec_q8_linear, dev, stream, desc, shape[0], xp, xsp, wp, wsp, yp,
-          workspace.data_ptr(), workspace.nbytes)
+    lib = _q8_lib or _lib()
+    shape, dev, K, N, flags = xq.shape, xq.get_device(), desc.d_in, desc.d_out, desc.flags
+    rows = 2 * N if flags & SPEAR_EC_Q8_GATED else N
+    T = shape[0] if len(shape) else -1
+    if xq.dtype is not _int8 or wq.dtype is not _int8 or xs.dtype is not _f32 or ws.dtype is not _f32 or \
+            shape != (T, K) or wq.shape != (rows, K) or xs.shape != (T,) or ws.shape != (rows,) or \
+            wq.get_device() != dev or xs.get_device() != dev or ws.get_device() != dev or \
+            not xq.is_contiguous() or not wq.is_contiguous() or not xs.is_contiguous() or not ws.is_contiguous():
+        raise ValueError(f"xq must be int8 [tokens, {K}], wq int8 [{rows}, {K}] and their scales fp32 with an "
+                         "element a row, contiguous on one device")
+    if y.dtype is not (_f32 if flags & SPEAR_EC_OUT_F32 else _bf16) or y.shape != (T, N) or \
+            y.get_device() != dev or not y.is_contiguous():
+        raise ValueError(f"y must be contiguous of shape [{T}, {N}], bf16 or with out_f32 fp32, on xq's device")
+    if workspace is None or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous, on xq's device")
+    _run(lib.spear_ec_q8_linear, dev, stream, desc, T, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+         y.data_ptr(), workspace.data_ptr(), workspace.nbytes)
