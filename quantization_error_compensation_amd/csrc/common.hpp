@@ -290,8 +290,11 @@ __device__ __forceinline__ u32x4 bload16_dev(rsrc_t r, uint32_t voff, uint32_t s
 __device__ __forceinline__ void bstore_dev(rsrc_t r, uint32_t voff, uint32_t soff, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, voff, soff, kDeviceScope);
 }
-__device__ __forceinline__ void bstore16_dev(rsrc_t r, uint32_t voff, uint32_t soff, f32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, voff, soff, kDeviceScope);
+// No scalar offset: with one the compiler takes the data of a wide store as read
+// at once and may let the next instruction overwrite a register of it, which
+// then arrives in memory in its place (seen for lanes 12 to 15 of each 16).
+__device__ __forceinline__ void bstore16_dev(rsrc_t r, uint32_t voff, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, voff, 0, kDeviceScope);
 }
 
 // Plain global loads from a wave-uniform base plus a 32-bit byte offset (the

@@ -646,7 +646,7 @@ __device__ __forceinline__ void put_part(const DecodeParams& p, int slot, int co
   const rsrc_t r = part_rsrc(p);
   for (int mt = 0; mt < MT; ++mt) {
     const int t = 16 * mt + 4 * q;
-    if (t < p.T) bstore16_dev(r, part_off(p, slot, col, t), 0, v[mt]);
+    if (t < p.T) bstore16_dev(r, part_off(p, slot, col, t), v[mt]);
   }
 }
 

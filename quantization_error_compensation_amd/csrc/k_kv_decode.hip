@@ -110,7 +110,7 @@ __device__ __forceinline__ float times_scale(float v, const u32x4 (&s)[2][2], in
 template <int N>
 __device__ __forceinline__ void store_piece(rsrc_t rs, uint32_t at, const float (&v)[N]) {
   if constexpr (N == 4)
-    bstore16_dev(rs, at, 0, f32x4{v[0], v[1], v[2], v[3]});
+    bstore16_dev(rs, at, f32x4{v[0], v[1], v[2], v[3]});
   else
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])}, rs, at, 0,
                                           kDeviceScope);

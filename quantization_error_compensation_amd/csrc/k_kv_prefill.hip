@@ -705,7 +705,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_attention_kernel(KvShape 
     for (int i = 0; i < D / 32; ++i)
       #pragma unroll
       for (int r = 0; r < 16; r += 4)
-        bstore16_dev(rs, ((8 * i + (r >> 1) + half) * kTileRows + me) * 16, 0,
+        bstore16_dev(rs, ((8 * i + (r >> 1) + half) * kTileRows + me) * 16,
                      f32x4{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]});
     if (half == 0) {
       bstore_dev(rs, kAtM + me * 4, 0, m);

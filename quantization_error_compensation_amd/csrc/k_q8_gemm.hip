@@ -12,7 +12,7 @@ struct TileParams {
   const float *xs, *ws;
   void* y;
   float* part;  // [tile][split][wave][16-byte piece][lane] partial sums
-  int* ctr;     // arrivals per tile
+  int* ctr;     // [tile][wave][32 tokens] arrivals
   int T, K, N, tiles_m, tiles_n, splits;
   int gelu, out_f32;
 };
@@ -55,7 +55,6 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
   constexpr int kParts = GATED ? 2 : 1, kCols = BN / kParts;  // columns of y
   static_assert(NT % kParts == 0, "a wave holds both projections of its columns");
   __shared__ __attribute__((aligned(128))) uint8_t smem[L::kLds];
-  __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int wm = wave / L::WN, wn = wave % L::WN;
   const int i32 = lane & 31, h = lane >> 5;
@@ -202,41 +201,57 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();  // every load has landed and every stage is read
 
-  // Split K: the last split of a tile to arrive adds the others' sums to its own.
+  // Split K.  A wave's sums meet those of the same wave of the tile's other
+  // splits, one part (32 tokens) after the other: it stores a part, waits until
+  // it has arrived and counts it; whoever counts a part last adds the others' to
+  // its own, which are still in registers, and finishes that part.  No one
+  // waits for another.  The splits take the parts in turned order, so that each
+  // is likely to come last to other parts than the rest.
+  uint32_t finish = (1u << MT) - 1;  // the parts that this wave finishes
   if (p.splits > 1) {
-    constexpr int kFloats = BM * BN;
+    constexpr int kFloats = BM * BN, kPartBytes = NT * 4 * 1024;
     const rsrc_t pr = make_rsrc(p.part + (size_t)tile * p.splits * kFloats, (uint32_t)p.splits * kFloats * 4);
-    const uint32_t mine = (uint32_t)(wave * NT * MT * 16 * 64 + lane * 4) * 4;
+    const uint32_t mine = (uint32_t)wave * (NT * MT * 4096) + lane * 16;
+    int* ctr = p.ctr + (tile * L::kWaves + wave) * MT;
+    const int first = split * MT / p.splits;
+    finish = 0;
+    for (int j = 1; j <= MT; ++j) {
+      const int part = first + j < MT ? first + j : first + j - MT;
+      #pragma unroll
+      for (int b = 0; b < MT; ++b) {
+        if (b != part) continue;
+        #pragma unroll
+        for (int a = 0; a < NT; ++a)
+          #pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const i32x4 v = {acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
+            bstore16_dev(pr, mine + (uint32_t)split * kFloats * 4 + b * kPartBytes + (a * 4 + g) * 1024,
+                         __builtin_bit_cast(f32x4, v));
+          }
+      }
+      wait_vmem();
+      int seen = 0;
+      if (lane == 0) seen = atomicAdd(ctr + part, 1);
+      if (__builtin_amdgcn_readfirstlane(seen) == p.splits - 1) finish |= 1u << part;
+    }
     #pragma unroll
-    for (int a = 0; a < NT; ++a)
-      #pragma unroll
-      for (int b = 0; b < MT; ++b)
+    for (int b = 0; b < MT; ++b) {
+      if (!(finish >> b & 1)) continue;
+      if (lane == 0) store_dev(ctr + b, 0);
+      for (int o = 0; o < p.splits; ++o) {
+        if (o == split) continue;
         #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const i32x4 v = {acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
-          bstore16_dev(pr, mine + ((a * MT + b) * 4 + g) * 1024, (uint32_t)split * kFloats * 4,
-                       __builtin_bit_cast(f32x4, v));
-        }
-    wait_vmem();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(&p.ctr[kCtrTile + tile], 1) == p.splits - 1;
-    __syncthreads();
-    if (!s_last) return;
-    if (threadIdx.x == 0) store_dev(&p.ctr[kCtrTile + tile], 0);
-    for (int o = 0; o < p.splits; ++o) {
-      if (o == split) continue;
-      #pragma unroll
-      for (int a = 0; a < NT; ++a)
-        #pragma unroll
-        for (int b = 0; b < MT; ++b)
+        for (int a = 0; a < NT; ++a)
           #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const i32x4 v = __builtin_bit_cast(
-                i32x4, bload16_dev(pr, mine + ((a * MT + b) * 4 + g) * 1024, (uint32_t)o * kFloats * 4));
+                i32x4, bload16_dev(pr, mine + b * kPartBytes + (a * 4 + g) * 1024, (uint32_t)o * kFloats * 4));
             #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[a][b][4 * g + j] += v[j];
+            for (int k = 0; k < 4; ++k) acc[a][b][4 * g + k] += v[k];
           }
+      }
     }
+    if (!finish) return;
   }
 
   // A lane holds token i32 of a block and weight rows 8 g + 4 h + 0 .. 3.
@@ -260,7 +275,8 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
   const int c0 = n0 + wn * NC * 32, t0 = m0 + wm * MT * 32;
   if (p.out_f32) {
     #pragma unroll
-    for (int b = 0; b < MT; ++b)
+    for (int b = 0; b < MT; ++b) {
+      if (!(finish >> b & 1)) continue;
       #pragma unroll
       for (int a = 0; a < NC; ++a)
         #pragma unroll
@@ -270,32 +286,35 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
           if (t < p.T && n < p.N)
             *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + (size_t)t * p.N + n) = o;
         }
+    }
     return;
   }
   // Through LDS, a part of the ring for each wave, so that rows of y are
   // written as whole 64- or 128-byte runs: stored as the lanes hold them (8
   // bytes of 32 rows at a time) the results cost a third of the kernel's time.
   constexpr int kPieces = NC * 4, kShare = 16 / kPieces;  // 16-byte pieces of a row, rows of 256 bytes
-  uint8_t* own = smem + wave * (MT * 32 * kPieces * 16);
+  uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t0 * p.N + c0;
+  const int live = p.T - t0, cols = p.N - c0;
   #pragma unroll
-  for (int b = 0; b < MT; ++b)
+  for (int b = 0; b < MT; ++b) {
+    if (!(finish >> b & 1)) continue;
+    uint8_t* own = smem + (wave * MT + b) * (32 * kPieces * 16);
     #pragma unroll
     for (int a = 0; a < NC; ++a)
       #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4 o = result(a, b, g);
         const int piece = (a * 4 + g) ^ ((i32 / kShare) & (kPieces - 1));
-        *reinterpret_cast<u32x2*>(own + (b * 32 + i32) * kPieces * 16 + piece * 16 + 8 * h) =
+        *reinterpret_cast<u32x2*>(own + i32 * kPieces * 16 + piece * 16 + 8 * h) =
             u32x2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
       }
-  uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t0 * p.N + c0;
-  const int live = p.T - t0, cols = p.N - c0;
-  #pragma unroll
-  for (int j = 0; j < MT * 32 * kPieces / 64; ++j) {
-    const int r = j * (64 / kPieces) + lane / kPieces;
-    const int col = ((lane % kPieces) ^ ((r / kShare) & (kPieces - 1))) * 8;
-    const u32x4 d = *reinterpret_cast<const u32x4*>(own + j * 1024 + lane * 16);
-    if (r < live && col < cols) *reinterpret_cast<u32x4*>(y + (size_t)r * p.N + col) = d;
+    #pragma unroll
+    for (int j = 0; j < kPieces / 2; ++j) {
+      const int r = j * (64 / kPieces) + lane / kPieces;
+      const int col = ((lane % kPieces) ^ ((r / kShare) & (kPieces - 1))) * 8;
+      const u32x4 d = *reinterpret_cast<const u32x4*>(own + j * 1024 + lane * 16);
+      if (b * 32 + r < live && col < cols) *reinterpret_cast<u32x4*>(y + (size_t)(b * 32 + r) * p.N + col) = d;
+    }
   }
 }
 
@@ -348,11 +367,12 @@ hipError_t launch_q8_product(const Q8Shape& s, const Q8Product& a, void* workspa
   switch (pl.tile) {
     case 0: return launch_shape<Tile<256, 256, 2, 4, 128, 2>, 0>(s, a, pl.splits, workspace, st);
     case 1: return launch_shape<Tile<192, 256, 2, 4, 128, 2>, 1>(s, a, pl.splits, workspace, st);
-    case 2: return launch_shape<Tile<128, 256, 2, 4, 128, 3>, 2>(s, a, pl.splits, workspace, st);
-    case 3: return launch_shape<Tile<128, 128, 2, 4, 128, 4>, 3>(s, a, pl.splits, workspace, st);
-    case 4: return launch_shape<Tile<64, 128, 2, 2, 128, 3>, 4>(s, a, pl.splits, workspace, st);
-    case 5: return launch_shape<Tile<64, 64, 2, 2, 128, 4>, 5>(s, a, pl.splits, workspace, st);
-    default: return launch_shape<Tile<32, 128, 1, 4, 128, 3>, 6>(s, a, pl.splits, workspace, st);
+    case 2: return launch_shape<Tile<256, 128, 4, 2, 128, 3>, 2>(s, a, pl.splits, workspace, st);
+    case 3: return launch_shape<Tile<128, 256, 2, 4, 128, 3>, 3>(s, a, pl.splits, workspace, st);
+    case 4: return launch_shape<Tile<128, 128, 2, 4, 128, 4>, 4>(s, a, pl.splits, workspace, st);
+    case 5: return launch_shape<Tile<64, 128, 2, 2, 128, 3>, 5>(s, a, pl.splits, workspace, st);
+    case 6: return launch_shape<Tile<64, 64, 2, 2, 128, 4>, 6>(s, a, pl.splits, workspace, st);
+    default: return launch_shape<Tile<32, 128, 1, 4, 128, 3>, 7>(s, a, pl.splits, workspace, st);
   }
 }
 

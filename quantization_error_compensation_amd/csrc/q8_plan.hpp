@@ -15,8 +15,8 @@
 namespace spear {
 
 constexpr int kQ8Units = 256;            // compute units of gfx950
-constexpr int kQ8CounterBytes = 16384;   // arrival counters at the head of the workspace
-constexpr int kQ8MaxSplitTiles = 1024;   // of them tiles' arrivals
+constexpr int kQ8CounterBytes = 65536;   // arrival counters at the head of the workspace
+constexpr int kQ8MaxSplitTiles = 512;    // each tile with up to 8 waves of 4 parts
 constexpr int64_t kQ8MaxPartials = (int64_t)64 << 20;
 constexpr int kQ8MaxSplits = 8;
 
@@ -62,20 +62,18 @@ inline Q8Stream plan_q8_stream(const Q8Shape& s) {
 }
 
 // ------------------------------------------------------------ many tokens
-// The tile kernel's shapes: tokens x weight rows, waves, LDS of a workgroup
-// decides how many of them a compute unit holds; block: us that a unit needs
-// for 128 codes of K of a tile, once: us that a tile's start and end add.
-// (Fitted to 1400 timings of 16 layers at 24 to 4096 tokens; the rule's choice
-// is 1.1% slower than the best of them on average.)
+// The tile kernel's shapes: tokens x weight rows; held: workgroups that a
+// compute unit holds; block: us that a unit needs for 128 codes of K of a tile;
+// once: us that a tile's start and end add.
 struct Q8Tile {
-  int bm, bn, held;  // held: workgroups a unit
-  bool gated;        // a wave holds both projections of its columns
+  int bm, bn, held;
+  bool gated;  // a wave holds both projections of its columns
   double block, once;
 };
 constexpr Q8Tile kQ8Tiles[] = {
-    {256, 256, 1, true, 1.33, 5.4}, {192, 256, 1, true, 1.15, 3.5}, {128, 256, 1, true, 0.75, 3.4},
-    {128, 128, 1, false, 0.45, 3.1}, {64, 128, 2, true, 0.29, 3.5}, {64, 64, 2, false, 0.175, 3.4},
-    {32, 128, 2, false, 0.21, 3.1}};
+    {256, 256, 1, true, 1.30, 2.2},  {192, 256, 1, true, 1.20, 2.0},   {256, 128, 1, true, 0.73, 2.1},
+    {128, 256, 1, true, 0.765, 2.2}, {128, 128, 1, false, 0.46, 2.4},  {64, 128, 2, true, 0.30, 3.3},
+    {64, 64, 2, false, 0.19, 3.1},   {32, 128, 2, false, 0.235, 2.9}};
 constexpr int kQ8TileCount = sizeof(kQ8Tiles) / sizeof(kQ8Tiles[0]);
 
 struct Q8TilePlan {
@@ -89,18 +87,22 @@ inline int64_t q8_tiles(const Q8Shape& s, const Q8Tile& t) {
 }
 
 // The shape and the number of splits of K with the least estimated time: the
-// fullest unit's tiles, the part of the memory traffic that does not hide behind
-// them (as if at 10 TB/s), and the partial sums' way through memory.  Splits
-// fill the units where tiles are few: 28672->8192 at 512 tokens, 256 x 128 tiles
-// of 128 x 256, 124 us with 2 splits (each unit half a tile's K), 128 x 128
-// without splits 144; 8192x8192 at 256 tokens 29.5 with 2 splits of 128 x 128,
-// 33.6 with 64 x 128 and none.
+// fullest unit's tiles, the memory traffic that does not hide behind them (as
+// if at 10.6 TB/s), and with splits the partial sums' way through memory.  The
+// constants are fitted to 3600 timings of 12 layers at 40 to 4096 tokens; the
+// choice is 0.9% slower than the best of them on average, 15% at worst.  What
+// it weighs, in us: large tiles fetch fewer bytes a product (3999 tokens gated
+// 8192->28672: 1470 with 256 x 256, 1640 with 128 x 256, 2060 with 64 x 128);
+// small ones fill the units (512 tokens 4096x4096: 14.6 with 64 x 128, 26 with
+// 256 x 128), and so do splits (512 tokens 28672->8192: 119 with 256 x 128 in 2,
+// 144 with 128 x 128 in 1; 256 tokens 8192x8192: 29 with 128 x 128 in 2, 34 with
+// 64 x 128 in 1).
 inline Q8TilePlan plan_q8_tiles(const Q8Shape& s) {
   Q8TilePlan best{0, 1, q8_tiles(s, kQ8Tiles[0])};
   double least = 1e300;
   const int blocks = (s.K + 127) / 128;
   const double rows = s.gated ? 2.0 * s.N : s.N;
-  const double memory = (rows * s.K + (double)s.T * s.K + 2.0 * s.T * s.N) / 10e6;
+  const double memory = (rows * s.K + (double)s.T * s.K + 2.0 * s.T * s.N) / 10.6e6;
   for (int i = 0; i < kQ8TileCount; ++i) {
     const Q8Tile& t = kQ8Tiles[i];
     if (s.gated && !t.gated) continue;
@@ -108,13 +110,16 @@ inline Q8TilePlan plan_q8_tiles(const Q8Shape& s) {
     if (i > 0 && tiles > 1 << 22) continue;  // a launch holds fewer than 2^32 threads
     for (int splits = 1; splits <= kQ8MaxSplits && splits <= blocks; ++splits) {
       if (splits > 1 && (tiles > kQ8MaxSplitTiles || tiles * splits * t.bm * t.bn * 4 > kQ8MaxPartials ||
-                         (t.bm * t.bn > 128 * 256 && splits > 2)))
+                         (t.bm * t.bn > 256 * 128 && splits > 4)))
         break;
       const int64_t each = (tiles * splits + kQ8Units - 1) / kQ8Units;
       double us = (double)each * ((blocks + splits - 1) / splits) * t.block + memory +
                   (double)((each + t.held - 1) / t.held) * t.once;
-      if (splits > 1)
-        us += 0.2 + 0.6 * splits + (0.45 * (splits - 1) + 1.4) * (double)each * t.bm * t.bn / 16384;
+      if (splits > 1) {
+        const double area = t.bm * t.bn;
+        us += 0.35 + 0.57 * splits + 0.09 * (splits - 1) * (double)each * area / 16384 +
+              0.19 * (double)(tiles * splits) * area * 4e-6;
+      }
       if (us < least) {
         least = us;
         best = Q8TilePlan{i, splits, tiles};
