@@ -136,6 +136,15 @@ __device__ __forceinline__ uint32_t four(const uint32_t* w) {
   const uint32_t high = __builtin_amdgcn_perm(w[3], w[2], 0x0C0C0400u);
   return low | high << 16;
 }
+// The same for a p of 24 significant bits, whose ratio to s may be a tie that
+// the product with the reciprocal misses: border is set where the product, off
+// by 2^-45 at most, is that near to one.  (Dividing every element instead:
+// 11008 x 4096 from memory 62 us, so 54 to 57.)
+__device__ __forceinline__ uint32_t code_or_border(float p, double inv, bool& border) {
+  const double ratio = (double)p * inv, rounded = ratio + kRoundMagic;
+  border |= fabs(fabs(ratio - (rounded - kRoundMagic)) - 0.5) < 0x1p-40;
+  return (uint32_t)__double2loint(rounded);
+}
 // The code of a value u as defined.
 __device__ __forceinline__ uint32_t code_as_defined(double u, double s) {
   return (uint32_t)(int)fmin(fmax(rint(u / s), -127.0), 127.0);
@@ -218,10 +227,15 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void quantize_kernel(const void
       const int i = at.lane + c * at.lanes;
       if (i >= pieces) continue;
       uint32_t code[8];
+      bool again = small;
       #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (F32 || small) code[j] = code_as_defined((double)value(c, j), (double)s);
+        if constexpr (F32) code[j] = code_or_border(value(c, j), inv, again);
         else code[j] = code_of(value(c, j), inv);
+      }
+      if (again) {
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) code[j] = code_as_defined((double)value(c, j), (double)s);
       }
       u32x2 out = {four(code), four(code + 4)};
       if (!good) out = u32x2{0, 0};
@@ -368,19 +382,20 @@ struct RowPlan {
 // A wave or part of it up to 256 pieces (2048 elements): 30000 rows of 1040 take
 // 39 us with 3 pieces a lane of a wave, 46 with two waves a row.  Wider rows
 // take the fewest waves of 2, 4, 8, 12, 16 that leave a thread at most 4 pieces,
-// or 2 in calls of fewer than 2048 rows, where a row's own time counts: waves
+// or 2 for fp32 (8192 x 4096 28 us, with 4 pieces 30) and in calls of fewer than
+// 2048 rows, where a row's own time counts: waves
 // that are no such number load the SIMDs unevenly, more pieces take registers
 // from a second workgroup, fewer leave lanes idle.  Norm with residual, us:
 //   8192 x 4096  2 waves of 4 pieces 37, 8 of 1 46     512 x 4096  4 waves of 2 5.5, 2 of 4 6.6
 //   4096 x 8192  4 of 4 37, 8 of 2 39, 6 of 3 48, 5 of 4 52
 //   3000 x 11008 8 of 3 38, 6 of 4 45, 4 of 6 45, 12 of 2 51
 //   2000 x 28672 12 of 5 93, 16 of 4 95, 8 of 7 103, 10 of 6 111
-RowPlan plan_rows(int rows, int pieces) {
+RowPlan plan_rows(int rows, int pieces, bool f32) {
   if (pieces <= 256) {
     const int lanes = pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
     return RowPlan{(pieces + lanes - 1) / lanes, lanes, 256, 256 / lanes};
   }
-  const int most = rows >= 2048 ? 4 : 2;
+  const int most = rows >= 2048 && !f32 ? 4 : 2;
   int threads = 1024;
   for (int t : {128, 256, 512, 768}) {
     if ((pieces + t - 1) / t > most) continue;
@@ -392,8 +407,8 @@ RowPlan plan_rows(int rows, int pieces) {
 constexpr int kMaxGrid = 65536;
 
 template <typename F>
-hipError_t with_plan(int rows, int width, F launch) {
-  const RowPlan pl = plan_rows(rows, width / 8);
+hipError_t with_plan(int rows, int width, bool f32, F launch) {
+  const RowPlan pl = plan_rows(rows, width / 8, f32);
   const int groups = (int)(((int64_t)rows + pl.rows - 1) / pl.rows);
   const dim3 grid(groups < kMaxGrid ? groups : kMaxGrid), block(pl.threads);
   switch (pl.c * 100 + pl.lanes) {
@@ -441,11 +456,11 @@ struct NormLaunch {
 
 hipError_t launch_q8_quantize(int rows, int width, const void* x, bool x_f32, int64_t x_stride,
                               int8_t* codes, float* scales, hipStream_t st) {
-  return with_plan(rows, width, QuantizeLaunch{rows, width, x, x_f32, x_stride, codes, scales, st});
+  return with_plan(rows, width, x_f32, QuantizeLaunch{rows, width, x, x_f32, x_stride, codes, scales, st});
 }
 
 hipError_t launch_q8_norm(int rows, int width, const Q8Norm& a, hipStream_t st) {
-  return with_plan(rows, width, NormLaunch{rows, width, a, st});
+  return with_plan(rows, width, false, NormLaunch{rows, width, a, st});
 }
 
 hipError_t launch_q8_dequant(int rows, int width, const int8_t* codes, const float* scales,

@@ -71,7 +71,7 @@ struct Q8Tile {
   double block, once;
 };
 constexpr Q8Tile kQ8Tiles[] = {
-    {256, 256, 1, true, 1.30, 2.2},  {192, 256, 1, true, 1.20, 2.0},   {256, 128, 1, true, 0.73, 2.1},
+    {256, 256, 1, true, 1.33, 2.2},  {192, 256, 1, true, 1.20, 2.0},   {256, 128, 1, true, 0.73, 2.1},
     {128, 256, 1, true, 0.765, 2.2}, {128, 128, 1, false, 0.46, 2.4},  {64, 128, 2, true, 0.30, 3.3},
     {64, 64, 2, false, 0.19, 3.1},   {32, 128, 2, false, 0.235, 2.9}};
 constexpr int kQ8TileCount = sizeof(kQ8Tiles) / sizeof(kQ8Tiles[0]);
