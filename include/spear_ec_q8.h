@@ -55,7 +55,8 @@ typedef struct spear_ec_q8_desc {
  * Quantize rows: x bf16, or fp32 with x_f32 != 0, row r at r * x_stride
  * elements (a multiple of 8, at least width), to codes int8 [rows][width] and
  * scales fp32 [rows].  For activations, and for weights (the rows of
- * [d_out][d_in]) when a model is loaded.  rows 0 launches nothing.
+ * [d_out][d_in]) when a model is loaded.  rows 0 launches nothing.  No output
+ * may overlap x or the other.
  */
 int spear_ec_q8_quantize(int32_t rows, int32_t width, const void* x, int32_t x_f32,
                          int64_t x_stride, int8_t* codes, float* scales, hipStream_t stream);
@@ -80,7 +81,7 @@ int spear_ec_q8_dequant_f32(int32_t rows, int32_t width, const int8_t* codes, co
  *            of y and codes is given
  * sum may be x (with x_stride == width) or residual itself; no other output
  * may overlap an input or another output.  The mean is held in 64 bits; y is off
- * by at most (1 + 2^-13) half steps of bf16, or by 2^-149 / sqrt(mean(h^2) + eps)
+ * by at most (1 + 2^-12) half steps of bf16, or by 2^-149 / sqrt(mean(h^2) + eps)
  * if that is more (products h * weight below fp32's normal range).  A row with
  * an infinity or NaN in h or in h * weight gets NaN throughout y, the scale NaN
  * and codes 0; so does one whose scale leaves fp32.
@@ -111,8 +112,8 @@ size_t spear_ec_q8_workspace_bytes(const spear_ec_q8_desc* desc, int32_t max_tok
  * depends on its own token and weight rows alone, bit for bit.  p takes three
  * fp32 roundings (the sum's conversion, times xs, times ws); where the sum times
  * xs leaves fp32's normal range so may p.  A bf16 y below 2^-126 may be zero.
- * act is computed in fp32, its sigmoid
- * within 2^-15 of itself where that is above 2^-126.
+ * act is computed in fp32, its sigmoid within 2^-15 of itself where that is
+ * above 2^-126.
  */
 int spear_ec_q8_linear(const spear_ec_q8_desc* desc, int32_t tokens, const int8_t* xq,
                        const float* xs, const int8_t* wq, const float* ws, void* y,

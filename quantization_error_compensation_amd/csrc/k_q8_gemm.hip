@@ -1,4 +1,30 @@
 // Products of the 8-bit path for many tokens: int8 codes on the matrix cores.
+//
+//     p[t][n] = xs[t] ws[n] sum_k cx[t][k] cw[n][k],   y = p or act(p_n) p_(n + N)
+//
+// A workgroup multiplies a tile of BM tokens with BN weight rows, K by 128
+// codes (one cache line of a row) through a ring of S stages in LDS, which
+// loads that write LDS directly fill.  The sums are 32-bit integers in
+// registers, exact for any order and split; scales and gate follow in fp32.
+// A gated tile holds 32 rows of one projection, the 32 of the other for the
+// same columns, and so on, so that a wave finds both in its own registers.
+//
+// Waves hold MT x NT results of the 32x32x32 instruction.  Operand reads take
+// LDS (MT + NT) / (MT NT) of the matrix time at 128 bytes a cycle, so the waves
+// are as square as eight of them can be; four waves of 128 x 128 would read a
+// third less, but one wave a SIMD shows every wait (2.0 against 2.45 PFLOP/s).
+// One half of the waves, one of each SIMD, issues all loads right after the
+// barrier while the other half computes, and computes when the other half is
+// done: a wave that issues loads does not issue matrix steps (gated, 3999
+// tokens 8192->28672: 1466 us, with every wave's own loads 1520 to 1575).
+//
+// What bounds it.  The largest products: the card's power.  4096 tokens of
+// 8192x8192 take 209 to 219 us (2.5 to 2.6 PFLOP/s; the library's int8 product
+// 2.1 here and 2.5 at best), the same on zeros 149 us, since the clock then
+// stays up.  Smaller tiles: loads into LDS, about 30 cycles a KB and unit when
+// they hit L2 and 41 from memory: a 128 x 256 tile waits 1500 to 2000 cycles for
+// 1024 of matrix steps.  Prefetching lines into L2 with loads of their own costs
+// more of that same path than it saves (512 tokens 28672->8192: 121 -> 127 us).
 #include "common.hpp"
 #include "internal.hpp"
 #include "q8_math.hpp"
@@ -17,10 +43,12 @@ struct TileParams {
   int gelu, out_f32;
 };
 
-constexpr int kDeep = 4;  // token tiles side by side in a run of tiles
+// Token tiles side by side in a run of tiles: 4096 tokens of 8192x8192 277 us with
+// 1, 235 with 2, 232 with 4 and 8, 265 with 16 (before the results went through
+// LDS).
+constexpr int kDeep = 4;
 
-// BM tokens x BN weight rows a workgroup, WM x WN waves, K by BK codes through
-// a ring of S stages.
+// BM tokens x BN weight rows a workgroup, WM x WN waves, K by BK codes, S stages.
 template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
@@ -291,7 +319,7 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
   }
   // Through LDS, a part of the ring for each wave, so that rows of y are
   // written as whole 64- or 128-byte runs: stored as the lanes hold them (8
-  // bytes of 32 rows at a time) the results cost a third of the kernel's time.
+  // bytes of 32 rows at a time) they cost 4096 tokens of 8192x8192 235 us, not 211.
   constexpr int kPieces = NC * 4, kShare = 16 / kPieces;  // 16-byte pieces of a row, rows of 256 bytes
   uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t0 * p.N + c0;
   const int live = p.T - t0, cols = p.N - c0;

