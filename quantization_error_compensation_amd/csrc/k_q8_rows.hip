@@ -308,8 +308,9 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
     bool good = top < kInfBits && squares < 1e300;
     const double m = (double)__uint_as_float(top);
     float s = scale_of(m * r);
-    // near fp32's small end the products are taken again, in fp64
-    const bool small = good && (m < kSmallMax || s < kSmallScale);
+    // near fp32's small end the products are taken again, in fp64; not for a row
+    // of zeros (padding: 4096 x 8192 of them 102 us, so 32), whose products are exact
+    const bool small = good && squares > 0 && (m < kSmallMax || s < kSmallScale);
     auto product = [&](int c, int j) {
       const int i = at.lane + c * at.lanes;
       if (i >= pieces) return 0.0;

@@ -208,6 +208,42 @@ def test_rows_that_are_not_finite(torch, ref):
     assert torch.equal(out.isnan().all(1), bad) and torch.equal(out.isnan().any(1), bad)
 
 
+@pytest.mark.parametrize("width", [128, 1040, 8208])
+def test_norm_of_rows_of_zeros(torch, ref, width):
+    """Padding: rows of zeros (of either sign, or cancelled by the residual)
+    between others of every size give zeros and the scale 1, but NaN with a
+    weight that is not finite."""
+    note(f"zeros {width}")
+    g = rng(torch, width)
+    rows = 65
+    x = torch.randn(rows, width, generator=g, device="cuda").bfloat16()
+    r = torch.randn(rows, width, generator=g, device="cuda").bfloat16()
+    x[5::10] *= 2.0 ** -70
+    r[5::10] *= 2.0 ** -70
+    x[::3] = 0
+    r[::3] = torch.where(torch.rand(rows, width, generator=g, device="cuda") < 0.5, 0.0, -0.0).bfloat16()[::3]
+    r[1::6] = -x[1::6]
+    w = torch.randn(width, generator=g, device="cuda").bfloat16()
+    for last in (1.0, 0.0, math.inf, math.nan):
+        w[-1] = last
+        s, y = torch.empty_like(x), torch.empty_like(x)
+        codes, scales = q.alloc_q8(rows, width)
+        q.spear_ec_q8_rmsnorm(x, r, s, w, 1e-6, y, codes, scales)
+        h, u = ref.norm(x, r, w, 1e-6)
+        assert torch.equal(s, h)
+        zero = (h == 0).all(1)
+        assert zero.sum() >= 22
+        assert bool((codes[zero] == 0).all())
+        if math.isfinite(last):
+            assert bool((scales[zero] == 1).all()) and bool((y[zero] == 0).all())
+        else:
+            assert bool(scales[zero].isnan().all()) and bool(y[zero].isnan().all())
+        want_c, want_s = ref.quantize(u)
+        near = (u / want_s.double()[:, None]).abs().frac().sub(0.5).abs() < 2.0 ** -22
+        assert torch.allclose(scales, want_s, rtol=2.0 ** -23, atol=0, equal_nan=True)
+        assert bool(((codes == want_c) | (near & ((codes.int() - want_c.int()).abs() <= 1))).all())
+
+
 def test_norm_weights_and_eps_at_the_ends(torch, ref):
     """Weights and values whose products leave fp32's normal range, and large eps."""
     g = rng(torch, 9)
