@@ -16,7 +16,11 @@
 // One half of the waves, one of each SIMD, issues all loads right after the
 // barrier while the other half computes, and computes when the other half is
 // done: a wave that issues loads does not issue matrix steps (gated, 3999
-// tokens 8192->28672: 1466 us, with every wave's own loads 1520 to 1575).
+// tokens 8192->28672: 1466 us, with every wave's own loads 1520 to 1575).  Tiles
+// whose sums fit four waves beside four that load alone (256 x 128) read a quarter
+// less from LDS that way, which is power: 512 tokens 28672->8192 122 -> 118 us, on
+// zeros 102 and 103; with one tile of tokens, where loads bind, it is 2 to 6%
+// slower, and 128 x 256 gains nothing.
 //
 // What bounds it.  The largest products: the card's power.  4096 tokens of
 // 8192x8192 take 209 to 219 us (2.5 to 2.6 PFLOP/s; the library's int8 product
@@ -24,7 +28,7 @@
 // stays up.  Smaller tiles: loads into LDS, about 30 cycles a KB and unit when
 // they hit L2 and 41 from memory: a 128 x 256 tile waits 1500 to 2000 cycles for
 // 1024 of matrix steps.  Prefetching lines into L2 with loads of their own costs
-// more of that same path than it saves (512 tokens 28672->8192: 121 -> 127 us).
+// more of that same path than it saves (512 tokens 28672->8192, then: 121 -> 127 us).
 #include "common.hpp"
 #include "internal.hpp"
 #include "q8_math.hpp"
@@ -48,14 +52,16 @@ struct TileParams {
 // LDS).
 constexpr int kDeep = 4;
 
-// BM tokens x BN weight rows a workgroup, WM x WN waves, K by BK codes, S stages.
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_>
+// BM tokens x BN weight rows a workgroup, WM x WN waves, K by BK codes, S stages,
+// D waves more that only load.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, int D_ = 0>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
-  static constexpr int kWaves = WM * WN;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_, D = D_;
+  static constexpr int kWaves = WM * WN, kAll = kWaves + D;
   static constexpr int MT = BM / WM / 32, NT = BN / WN / 32;  // 32 x 32 results of a wave
-  // The first half of the waves, one on each SIMD, issues every load.
-  static constexpr int kLoaders = kWaves > 4 ? kWaves / 2 : kWaves;
+  // The first half of the waves, one on each SIMD, issues every load, or the last D do.
+  static constexpr int kFirstLoader = D ? kWaves : 0;
+  static constexpr int kLoaders = D ? D : kWaves > 4 ? kWaves / 2 : kWaves;
   static constexpr int kRowsPerLoad = 1024 / BK;
   static constexpr int kXLoads = BM / kRowsPerLoad / kLoaders, kWLoads = BN / kRowsPerLoad / kLoaders;
   static constexpr int kLoads = kXLoads + kWLoads;
@@ -77,7 +83,7 @@ __device__ __forceinline__ int swizzle(int row) {
 }
 
 template <typename L, bool GATED>
-__global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
+__global__ __launch_bounds__(64 * L::kAll, 1) void tile_kernel(TileParams p) {
   constexpr int BM = L::BM, BN = L::BN, BK = L::BK, S = L::S, MT = L::MT, NT = L::NT;
   constexpr int kSteps = BK / 32;
   constexpr int kParts = GATED ? 2 : 1, kCols = BN / kParts;  // columns of y
@@ -115,7 +121,7 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
     const u32x4 sx = sdesc(p.xs + m0, (uint32_t)rows_m * 4);
     const u32x4 sw = sdesc(p.ws + n0, (uint32_t)rows_n * 4);
     const u32x4 su = GATED ? sdesc(p.ws + p.N + n0, (uint32_t)rows_n * 4) : sw;
-    for (int c = wave; c < (BM + BN) / 32; c += L::kWaves) {  // 32 at a time, by half a wave
+    for (int c = wave; c < (BM + BN) / 32; c += L::kAll) {  // 32 at a time, by half a wave
       const int f = c * 32 - BM;
       const uint32_t to = lds0 + L::kRing + c * 128;
       if (lane < 32) {
@@ -130,18 +136,18 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
   // of the weights' stage: 32 of y's columns, with GATED the other
   // projection's for the same columns behind them.
   constexpr int R = L::kRowsPerLoad, P = BK / 16;
-  const int lr = lane / P, lp = lane % P;
+  const int lr = lane / P, lp = lane % P, lw = wave - L::kFirstLoader;
   uint32_t xoff[L::kXLoads], woff[L::kWLoads];  // at k = 0
   int xpiece[L::kXLoads];
   #pragma unroll
   for (int j = 0; j < L::kXLoads; ++j) {
-    const int r = (wave * L::kXLoads + j) * R + lr;
+    const int r = (lw * L::kXLoads + j) * R + lr;
     xpiece[j] = (lp ^ swizzle<BK>(r)) * 16;
     xoff[j] = (uint32_t)r * p.K + xpiece[j];
   }
   #pragma unroll
   for (int j = 0; j < L::kWLoads; ++j) {
-    const int r = (wave * L::kWLoads + j) * R + lr;
+    const int r = (lw * L::kWLoads + j) * R + lr;
     woff[j] = (uint32_t)(GATED ? (r >> 6) * 32 + (r & 31) : r) * p.K + (lp ^ swizzle<BK>(r)) * 16;
   }
   // Past K the tokens' codes are zeros (an offset out of range), so whatever
@@ -151,10 +157,10 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
     const int k0 = kb * BK;
     #pragma unroll
     for (int j = 0; j < L::kXLoads; ++j)
-      dma16(xr, to + (wave * L::kXLoads + j) * 1024, k0 + xpiece[j] < p.K ? xoff[j] + k0 : 0x80000000u);
+      dma16(xr, to + (lw * L::kXLoads + j) * 1024, k0 + xpiece[j] < p.K ? xoff[j] + k0 : 0x80000000u);
     #pragma unroll
     for (int j = 0; j < L::kWLoads; ++j) {
-      const int first = (wave * L::kWLoads + j) * R;
+      const int first = (lw * L::kWLoads + j) * R;
       const bool other = GATED && (first & 32);
       dma16(other ? ur : wr, to + BM * BK + first * BK, woff[j] + k0);
     }
@@ -190,7 +196,7 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
   // The order of the blocks is free (sums of integers): with one tile of tokens
   // every tile begins at another one, so that the rows' equal columns, which
   // lie a power of two apart, are not asked of the same memory channels at once.
-  const bool loader = wave < L::kLoaders;
+  const bool loader = lw >= 0 && lw < L::kLoaders;
   int next = kb0 + (p.tiles_m == 1 ? first_block(tn, kb1 - kb0) : 0);
   auto load_next = [&](int stage) {
     issue(next, stage);
@@ -200,18 +206,31 @@ __global__ __launch_bounds__(64 * L::kWaves, 1) void tile_kernel(TileParams p) {
     #pragma unroll
     for (int s = 0; s < S - 1; ++s) load_next(s);
   }
+  if (L::D > 0 && loader) {  // the same waits and barriers as below, and nothing else
+    for (int kb = kb0, into = S - 1; kb < kb1; ++kb) {
+      wait_vmcnt<(S - 2) * L::kLoads>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      load_next(into);
+      into = into + 1 == S ? 0 : into + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    return;
+  }
+  if (L::D > 0) wait_vmcnt<0>();  // this wave's share of the scales
   u32x4 wc[NT], xc[MT];  // the last step's operands
   for (int a = 0; a < NT; ++a) wc[a] = u32x4{0, 0, 0, 0};
   for (int b = 0; b < MT; ++b) xc[b] = u32x4{0, 0, 0, 0};
   int stage = 0, into = S - 1;
   for (int kb = kb0; kb < kb1; ++kb) {
-    wait_vmcnt<(S - 2) * L::kLoads>();
+    if (L::D == 0) wait_vmcnt<(S - 2) * L::kLoads>();
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     u32x4 w[2][NT], x[2][MT];
     read(stage, 0, w[0], x[0]);
-    if (loader) load_next(into);
+    if (L::D == 0 && loader) load_next(into);
     if (kb > kb0) step(wc, xc);
     #pragma unroll
     for (int s = 0; s + 1 < kSteps; ++s) {
@@ -365,7 +384,7 @@ hipError_t launch_tile(const Q8Shape& s, const Q8Product& a, int splits, void* w
   p.splits = splits;
   p.gelu = s.gelu;
   p.out_f32 = s.out_f32;
-  const dim3 grid(p.tiles_m * p.tiles_n * splits), block(64 * L::kWaves);
+  const dim3 grid(p.tiles_m * p.tiles_n * splits), block(64 * L::kAll);
   if (!s.gated)
     hipLaunchKernelGGL((tile_kernel<L, false>), grid, block, 0, st, p);
   else if constexpr (L::NT % 2 == 0)
@@ -395,7 +414,9 @@ hipError_t launch_q8_product(const Q8Shape& s, const Q8Product& a, void* workspa
   switch (pl.tile) {
     case 0: return launch_shape<Tile<256, 256, 2, 4, 128, 2>, 0>(s, a, pl.splits, workspace, st);
     case 1: return launch_shape<Tile<192, 256, 2, 4, 128, 2>, 1>(s, a, pl.splits, workspace, st);
-    case 2: return launch_shape<Tile<256, 128, 4, 2, 128, 3>, 2>(s, a, pl.splits, workspace, st);
+    case 2:
+      if (s.T > 256) return launch_shape<Tile<256, 128, 2, 2, 128, 3, 4>, 2>(s, a, pl.splits, workspace, st);
+      return launch_shape<Tile<256, 128, 4, 2, 128, 3>, 2>(s, a, pl.splits, workspace, st);
     case 3: return launch_shape<Tile<128, 256, 2, 4, 128, 3>, 3>(s, a, pl.splits, workspace, st);
     case 4: return launch_shape<Tile<128, 128, 2, 4, 128, 4>, 4>(s, a, pl.splits, workspace, st);
     case 5: return launch_shape<Tile<64, 128, 2, 2, 128, 3>, 5>(s, a, pl.splits, workspace, st);

@@ -97,7 +97,7 @@ inline int64_t q8_tiles(const Q8Shape& s, const Q8Tile& t) {
 // shapes much alike, so that the choice is the same.  What it weighs, in us: large tiles fetch fewer bytes a product (3999 tokens gated
 // 8192->28672: 1470 with 256 x 256, 1640 with 128 x 256, 2060 with 64 x 128);
 // small ones fill the units (512 tokens 4096x4096: 14.6 with 64 x 128, 26 with
-// 256 x 128), and so do splits (512 tokens 28672->8192: 119 with 256 x 128 in 2,
+// 256 x 128), and so do splits (512 tokens 28672->8192: 118 with 256 x 128 in 2,
 // 144 with 128 x 128 in 1; 256 tokens 8192x8192: 29 with 128 x 128 in 2, 34 with
 // 64 x 128 in 1).
 inline Q8TilePlan plan_q8_tiles(const Q8Shape& s) {

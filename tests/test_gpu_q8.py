@@ -299,7 +299,8 @@ def test_products(torch, ref, i, act):
 LARGE = [(1, 28672, 8192, "none"), (3, 11008, 4096, "none"), (1, 4096, 11008, "silu"), (20, 8192, 4112, "gelu"),
          (40, 65536, 1024, "none"), (64, 4096, 4096, "none"), (72, 8192, 7168, "silu"), (130, 28672, 1040, "none"),
          (320, 4096, 4096, "none"), (512, 28672, 2048, "none"), (777, 4112, 5536, "silu"), (2048, 4096, 4096, "none"),
-         (2500, 1024, 8192, "gelu"), (4099, 2064, 2064, "none"), (9000, 512, 512, "none")]
+         (2500, 1024, 8192, "gelu"), (4099, 2064, 2064, "none"), (9000, 512, 512, "none"),
+         (475, 20224, 3584, "none"), (1252, 9728, 1408, "silu"), (700, 20000, 528, "gelu")]
 
 
 @pytest.mark.parametrize("T,K,N,act", LARGE)
