@@ -363,7 +363,12 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
 
 // Four codes a thread and step: consecutive lanes write consecutive 16 bytes.
 // 2^share lanes of a workgroup take a row, so that narrow rows fill it too
-// (100000 rows of 128: 22 us with a workgroup for each, 11.5 so).
+// (100000 rows of 128: 22 us with a workgroup for each, 11.5 so).  The values, four
+// times as many bytes as the codes, are marked to leave the caches first: from
+// memory 4096 x 8192 33 -> 27 us, from the last-level cache the same.  The other
+// operators' results are read next; so marked, quantizing 11008 x 4096 and reading
+// it back takes 83 us instead of 73, norm and quantization of its bf16 result 48.6
+// instead of 47.
 __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__ codes,
                                                       const float* __restrict__ scales,
                                                       float* __restrict__ out, int rows, int width, int share) {
@@ -378,7 +383,7 @@ __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__
       f32x4 v;
       #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = (float)(int8_t)(c >> (8 * j)) * s;
-      to[i] = v;
+      __builtin_nontemporal_store(v, to + i);
     }
   }
 }
