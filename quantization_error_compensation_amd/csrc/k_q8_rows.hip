@@ -20,11 +20,11 @@
 // Rows of up to 2048 elements belong to one wave or, of up to 256, to a part
 // of one, and meet no barrier; wider ones to a workgroup.
 //
-// Norm with residual, 4096 x 8192: 40 us (5.9 TB/s), 53 with inputs and outputs
-// that the last-level cache does not hold (4.4 TB/s; a copy reaches 4.9); without
-// residual 22 us, where the fp64 steps of the sum and the codes show.
-// Quantization of bf16 4096 x 8192 18 us (5.6 TB/s), of fp32 11008 x 4096 42 to 55
-// us (5.4 to 4.1).  One row of 4096: 3.4 us, most of it launch, one load's latency
+// Norm with residual, 4096 x 8192: 40 us (5.9 TB/s), 43 to 46 with inputs and
+// outputs that the last-level cache does not hold (5.5 to 5.1 TB/s; a copy reaches
+// 4.9); without residual 22 us, where the fp64 steps of the sum and the codes show.
+// Quantization of bf16 4096 x 8192 18 us (5.6 TB/s), of fp32 11008 x 4096 38 to 41
+// us (5.9 to 5.5).  One row of 4096: 3.4 us, most of it launch, one load's latency
 // and the chain from the sums to the ratio.
 #include "common.hpp"
 #include "q8_math.hpp"
@@ -251,7 +251,14 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void quantize_kernel(const void
   }
 }
 
-template <int C, int LANES>
+// Stores 16 bytes; EARLY: marked to leave the caches first.
+template <bool EARLY>
+__device__ __forceinline__ void put(u32x4 v, u32x4* p) {
+  if constexpr (EARLY) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+template <int C, int LANES, bool EARLY>
 __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int rows, int width) {
   __shared__ uint64_t red[32];
   const RowTeam<LANES> team{red};
@@ -288,7 +295,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
         #pragma unroll
         for (int j = 0; j < 4; ++j)  // as one rounding: fp32's 24 bits are at least 2 * 8 + 2
           h[c][j] = rounded_pair(bf16_lo(h[c][j]) + bf16_lo(d[c][j]), bf16_hi(h[c][j]) + bf16_hi(d[c][j]));
-        if (live && i < pieces) sr[i] = h[c];
+        if (live && i < pieces) put<EARLY>(h[c], sr + i);
       }
     }
     float p[C][8];
@@ -355,7 +362,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
         u32x4 out;
         #pragma unroll
         for (int j = 0; j < 4; ++j) out[j] = good ? rounded_pair(y[2 * j], y[2 * j + 1]) : 0x7FC07FC0u;
-        reinterpret_cast<u32x4*>(a.y + (int64_t)row * width)[i] = out;
+        put<EARLY>(out, reinterpret_cast<u32x4*>(a.y + (int64_t)row * width) + i);
       }
     }
   }
@@ -365,10 +372,9 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
 // 2^share lanes of a workgroup take a row, so that narrow rows fill it too
 // (100000 rows of 128: 22 us with a workgroup for each, 11.5 so).  The values, four
 // times as many bytes as the codes, are marked to leave the caches first: from
-// memory 4096 x 8192 33 -> 27 us, from the last-level cache the same.  The other
-// operators' results are read next; so marked, quantizing 11008 x 4096 and reading
-// it back takes 83 us instead of 73, norm and quantization of its bf16 result 48.6
-// instead of 47.
+// memory 4096 x 8192 33 -> 27 us, from the last-level cache the same.  Codes are
+// read next: so marked, quantizing 11008 x 4096 and reading it back takes 83 us
+// instead of 73.
 __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__ codes,
                                                       const float* __restrict__ scales,
                                                       float* __restrict__ out, int rows, int width, int share) {
@@ -455,13 +461,25 @@ struct QuantizeLaunch {
   }
 };
 
+// Results that the L2s (32 MB in all) would hold until the kernel's end, and only
+// then write, leave it while the kernel runs.  That pays up to about 12 MB, the next
+// read of them included; past that the next read is slower by more.  us, without
+// and with, norm to bf16 alone, norm and a quantization of its result, two norms
+// that pass a residual on:
+//   512 x 8192 6.1 / 5.4, 11.0 / 10.7, 16.9 / 16.1    1333 x 4096 8.1 / 7.1, 13.1 / 12.4, 20.7 / 20.1
+//   1024 x 8192 10.0 / 9.3, 16.4 / 15.9, 26.7 / 27.4  4096 x 8192 28.1 / 24.9, 45.9 / 47.9, 83.6 / 86.4
+constexpr int64_t kEarly = 6 << 20;  // elements
+
 struct NormLaunch {
   int rows, width;
   const Q8Norm& a;
   hipStream_t st;
   template <int C, int LANES>
   void operator()(dim3 grid, dim3 block) const {
-    hipLaunchKernelGGL((norm_kernel<C, LANES>), grid, block, 0, st, a, rows, width);
+    if ((int64_t)rows * width <= kEarly)
+      hipLaunchKernelGGL((norm_kernel<C, LANES, true>), grid, block, 0, st, a, rows, width);
+    else
+      hipLaunchKernelGGL((norm_kernel<C, LANES, false>), grid, block, 0, st, a, rows, width);
   }
 };
 
