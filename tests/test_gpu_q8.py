@@ -161,6 +161,30 @@ def test_norm(torch, ref, rows, width, residual):
             ok()
 
 
+@pytest.mark.parametrize("rows,width", [(1529, 4112), (1531, 4112), (3000, 8208), (140000, 16400)])
+def test_norm_of_large_calls(torch, ref, rows, width):
+    """Either side of the size up to which results leave the caches early, rows of
+    several pieces a thread, and matrices of 4.6 GB: sampled rows."""
+    note(f"large norm {rows} x {width}")
+    g = rng(torch, rows)
+    x = torch.randn((rows, width), generator=g, device="cuda", dtype=torch.bfloat16)
+    r = torch.randn((rows, width), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(width, generator=g, device="cuda").bfloat16()
+    s, y = torch.empty_like(x), torch.empty_like(x)
+    codes, scales = q.alloc_q8(rows, width)
+    q.spear_ec_q8_rmsnorm(x, r, s, w, 1e-5, y, codes, scales)
+    for at in (slice(0, 3), slice(rows // 2, rows // 2 + 3), slice(65534, 65539), slice(130944, 130947),
+               slice(rows - 3, rows)):
+        h, u = ref.norm(x[at], r[at], w, 1e-5)
+        assert torch.equal(s[at], h), at
+        # y: (1 + 2^-12) half steps; bf16's own rounding is check's
+        ref.check(y[at], u, u.abs() * 2.0 ** -8 * 2.0 ** -12, at)
+        want_c, want_s = ref.quantize(u)
+        near = (u / want_s.double()[:, None]).abs().frac().sub(0.5).abs() < 2.0 ** -22
+        assert torch.allclose(scales[at], want_s, rtol=2.0 ** -23, atol=0), at
+        assert bool(((codes[at] == want_c) | (near & ((codes[at].int() - want_c.int()).abs() <= 1))).all()), at
+
+
 def test_norm_strides_and_in_place(torch, ref):
     g = rng(torch, 5)
     wide = torch.randn((37, 3 * 512), generator=g, device="cuda").bfloat16()
