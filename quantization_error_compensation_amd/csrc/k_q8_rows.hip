@@ -338,7 +338,10 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
     if (!live) continue;
     if (a.codes && at.lane == 0) a.scales[row] = s;
     const double ratio = r / (double)s;
+    // where mean + eps is below 2^-254 or above 2^252 no fp32 holds r with its 24
+    // bits: y is taken from the products in fp64 there too
     const float r32 = (float)r;
+    const bool wide = small || (good && !(r >= 0x1p-126 && r <= 0x1p127));
     #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = at.lane + c * at.lanes;
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
         float y[8];
         #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = p[c][j] * r32;
-        if (small)
+        if (wide)
           for (int j = 0; j < 8; ++j) y[j] = (float)(product(c, j) * r);
         u32x4 out;
         #pragma unroll
