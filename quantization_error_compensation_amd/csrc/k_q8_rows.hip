@@ -9,13 +9,13 @@
 //     s = RN_fp32(max|p| r / 127),  c_j = rint(p_j r / s),
 // so both are reduced at once.  p_j is exact in fp32 (8 x 8 significant bits);
 // as non-negative floats order like their bits, the maximum is one of integers,
-// in which NaN and infinity come out on top.  The sum of squares and the ratio
+// in which infinity and NaN come out on top.  The sum of squares and the ratio
 // r / s are held in fp64, as codes next to a border between two steps would
 // otherwise fall on the wrong side; one fp64 fma with 1.5 * 2^52 as its addend
 // multiplies, rounds half to even and leaves the integer in its low word.  Rows
 // whose maximum or scale is near fp32's small end (where p_j is no longer
-// exact, or s so coarse that codes exceed 127) take the definition as it
-// stands: fp64 products, a division and a clamp.
+// exact, or s so coarse that codes exceed 127), or whose products leave fp32,
+// take the definition as it stands: fp64 products, a division and a clamp.
 //
 // Rows of up to 2048 elements belong to one wave or, of up to 256, to a part
 // of one, and meet no barrier; wider ones to a workgroup.
@@ -312,12 +312,14 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
       }
     team.join2(top, squares);
     const double r = 1.0 / sqrt(squares / width + a.eps);
-    bool good = top < kInfBits && squares < 1e300;
+    bool good = squares < 1e300;  // h is finite
     const double m = (double)__uint_as_float(top);
     float s = scale_of(m * r);
-    // near fp32's small end the products are taken again, in fp64; not for a row
-    // of zeros (padding: 4096 x 8192 of them 102 us, so 32), whose products are exact
-    const bool small = good && squares > 0 && (m < kSmallMax || s < kSmallScale);
+    // near fp32's small end and where a product leaves fp32 (or a weight is not
+    // finite) the products are taken again, in fp64; not for a row of zeros
+    // (padding: 4096 x 8192 of them 102 us, so 32), whose products are exact
+    const bool again =
+        good && (top >= kInfBits || (squares > 0 && (m < kSmallMax || s < kSmallScale)));
     auto product = [&](int c, int j) {
       const int i = at.lane + c * at.lanes;
       if (i >= pieces) return 0.0;
@@ -325,7 +327,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
       return (double)__uint_as_float((uint32_t)hr[8 * i + j] << 16) *
              (double)__uint_as_float((uint32_t)a.weight[8 * i + j] << 16);
     };
-    if (small) {
+    if (again) {
       uint64_t most = 0;
       if (live)  // others' rows are being written
         for (int c = 0; c < C; ++c)
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
     // where mean + eps is below 2^-254 or above 2^252 no fp32 holds r with its 24
     // bits: y is taken from the products in fp64 there too
     const float r32 = (float)r;
-    const bool wide = small || (good && !(r >= 0x1p-126 && r <= 0x1p127));
+    const bool wide = again || (good && !(r >= 0x1p-126 && r <= 0x1p127));
     #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = at.lane + c * at.lanes;
@@ -350,7 +352,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
         uint32_t code[8];
         #pragma unroll
         for (int j = 0; j < 8; ++j) code[j] = code_of(p[c][j], ratio);
-        if (small)
+        if (again)
           for (int j = 0; j < 8; ++j) code[j] = code_as_defined(product(c, j) * r, (double)s);
         u32x2 out = {four(code), four(code + 4)};
         if (!good) out = u32x2{0, 0};

@@ -84,3 +84,45 @@ def test_results_for_every_eps(torch, ref, width, eps):  # noqa: F811
         h, u = defined(torch, x, x.flip(0), w, eps)
         check(torch, ref, (total, y, codes, scales), h, u)
         assert bool((y[zero & zero.flip(0)] == 0).all())
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,width", [(5, 48), (6, 400), (7, 1936), (12, 4112), (3, 65536)])
+def test_products_past_fp32(torch, ref, rows, width, residual):  # noqa: F811
+    """Rows of finite h whose products with finite weights leave fp32, among
+    ordinary rows, rows of zeros, rows that are not finite, in place too."""
+    note(f"products past fp32 {rows} x {width} residual={residual}")
+    g = rng(torch, rows + width)
+    for hs, ws, eps in ((1e25, 1e20, 1e-5), (1e37, 1e37, 1e-5), (1e20, 1e30, 1e30), (1e38, 1e3, 1e80)):
+        x = (torch.randn((rows, width), generator=g, device="cuda").clamp(-3, 3) * hs).bfloat16()
+        x[1] = torch.randn(width, generator=g, device="cuda").bfloat16()
+        if rows > 3:
+            x[2] = 0
+            x[3, width // 2] = math.inf
+        w = (torch.randn(width, generator=g, device="cuda").clamp(-3, 3) * ws).bfloat16()
+        r = (torch.randn((rows, width), generator=g, device="cuda") * 1e-3 * hs).bfloat16() if residual else None
+        if residual:
+            r[1:3] = 0
+        h, u = defined(torch, x, r, w, eps)
+        assert bool((h.float() * w.float()).isinf().any()) and bool(u[0].isfinite().all())
+        check(torch, ref, run(torch, x, r, w, eps), h, u)
+        if residual:
+            codes, scales = q.alloc_q8(rows, width)
+            q.spear_ec_q8_rmsnorm(x, r, r, w, eps, y := torch.empty_like(x), codes, scales)
+            check(torch, ref, (r, y, codes, scales), h, u)
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_weights_that_are_not_finite(torch, ref, bad):  # noqa: F811
+    g = rng(torch, 3)
+    for width in (16, 272, 1040, 8208):
+        x = torch.randn((5, width), generator=g, device="cuda").bfloat16()
+        x[1] = 0
+        x[2] *= 2.0 ** -120
+        x[3] *= 1e38
+        w = torch.randn(width, generator=g, device="cuda").bfloat16()
+        w[width // 2] = bad
+        h, u = defined(torch, x, None, w, 1e-5)
+        got = run(torch, x, None, w, 1e-5)
+        check(torch, ref, got, h, u)
+        assert bool(got[1].isnan().all()) and bool(got[3].isnan().all())
