@@ -83,6 +83,8 @@ def alloc_q8_workspace(desc, max_tokens, device="cuda"):
 
 
 def spear_ec_q8_workspace_bytes(desc, max_tokens: int) -> int:
+    if int(max_tokens) >> 31:   # ctypes would keep its low 32 bits, here and below
+        return 0
     return int(_lib().spear_ec_q8_workspace_bytes(ctypes.byref(desc), int(max_tokens)))
 
 
@@ -99,24 +101,33 @@ def _run(fn, dev, stream, *args):
         _call(fn, dev, stream, *args)
 
 
-def _strided(x, shape, name):
-    """Row stride of a matrix whose rows may be strided."""
-    if len(shape) != 2 or (shape[1] > 1 and x.stride(1) != 1):
+def _too_large():
+    raise ValueError("rows and columns must be fewer than 2^31")
+
+
+def _sizes(x, shape, name):
+    """Rows, columns and row stride of a matrix whose rows may be strided."""
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix with contiguous rows")
-    return x.stride(0) if shape[0] > 1 else shape[1]
+    rows, width = shape
+    if (rows | width) >> 31:
+        _too_large()
+    if width > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return rows, width, x.stride(0) if rows > 1 else width
 
 
 def spear_ec_q8_quantize(x, codes, scales, stream=None):
     """Quantize the rows of x (bf16 or fp32 [rows, width], rows may be strided)."""
     lib = _q8_lib or _lib()
     shape, dev, kind = x.shape, x.get_device(), x.dtype
-    stride = _strided(x, shape, "x")
+    rows, width, stride = _sizes(x, shape, "x")
     if (kind is not _bf16 and kind is not _f32) or codes.dtype is not _int8 or scales.dtype is not _f32 or \
             codes.shape != shape or scales.shape != shape[:1] or codes.get_device() != dev or \
             scales.get_device() != dev or not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError("x must be bf16 or fp32, codes contiguous int8 of x's shape and scales contiguous "
                          "fp32 with an element a row, on one device")
-    _run(lib.spear_ec_q8_quantize, dev, stream, shape[0], shape[1], x.data_ptr(), kind is _f32, stride,
+    _run(lib.spear_ec_q8_quantize, dev, stream, rows, width, x.data_ptr(), kind is _f32, stride,
          codes.data_ptr(), scales.data_ptr())
 
 
@@ -130,7 +141,10 @@ def spear_ec_q8_dequant_f32(codes, scales, out, stream=None):
             not out.is_contiguous():
         raise ValueError("codes must be a contiguous int8 matrix, scales fp32 with an element a row and out "
                          "fp32 of codes' shape, contiguous on one device")
-    _run(lib.spear_ec_q8_dequant_f32, dev, stream, shape[0], shape[1], codes.data_ptr(), scales.data_ptr(),
+    rows, width = shape
+    if (rows | width) >> 31:
+        _too_large()
+    _run(lib.spear_ec_q8_dequant_f32, dev, stream, rows, width, codes.data_ptr(), scales.data_ptr(),
          out.data_ptr())
 
 
@@ -148,7 +162,7 @@ def spear_ec_q8_rmsnorm(x, residual, sum, weight, eps, y=None, codes=None, scale
     be None); to y (bf16) and/or quantized to codes and scales."""
     lib = _q8_lib or _lib()
     shape, dev = x.shape, x.get_device()
-    stride = _strided(x, shape, "x")
+    rows, width, stride = _sizes(x, shape, "x")
     if x.dtype is not _bf16 or weight.dtype is not _bf16 or weight.shape != shape[1:] or \
             weight.get_device() != dev or not weight.is_contiguous():
         raise ValueError("x must be bf16 and weight contiguous bf16 with an element a column, on one device")
@@ -162,7 +176,7 @@ def spear_ec_q8_rmsnorm(x, residual, sum, weight, eps, y=None, codes=None, scale
         cp, sp = codes.data_ptr(), scales.data_ptr()
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales are given together or not at all")
-    _run(lib.spear_ec_q8_rmsnorm, dev, stream, shape[0], shape[1], x.data_ptr(), stride,
+    _run(lib.spear_ec_q8_rmsnorm, dev, stream, rows, width, x.data_ptr(), stride,
          _rows_like(residual, shape, dev, "residual"), _rows_like(sum, shape, dev, "sum"), weight.data_ptr(), eps,
          _rows_like(y, shape, dev, "y"), cp, sp)
 
@@ -186,5 +200,7 @@ def spear_ec_q8_linear(desc, xq, xs, wq, ws, y, workspace, stream=None):
         raise ValueError(f"y must be contiguous of shape [{T}, {N}], bf16 or with out_f32 fp32, on xq's device")
     if workspace is None or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous, on xq's device")
+    if T >> 31:
+        _too_large()
     _run(lib.spear_ec_q8_linear, dev, stream, desc, T, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
          y.data_ptr(), workspace.data_ptr(), workspace.nbytes)
