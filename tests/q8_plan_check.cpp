@@ -32,3 +32,15 @@ extern "C" int q8_plan_faults(int K, int N, int gated, int T, int largest) {
   if (p.tiles * p.splits * 512 >= (int64_t)1 << 32) return 7;
   return 0;
 }
+
+// Which kernel a product takes: a stream's loads of tokens * 100 + tiles * 10 +
+// waves, or 10000 + 100 * (the tile's index, its form with loading waves being
+// one of its own) + splits of K.
+extern "C" int q8_plan_kernel(int K, int N, int gated, int T) {
+  const Q8Shape s{K, N, T, gated != 0, false, false};
+  const Q8Stream f = plan_q8_stream(s);
+  if (f.x) return f.x * 100 + f.tiles * 10 + f.waves;
+  const Q8TilePlan p = plan_q8_tiles(s);
+  const bool loading_waves = kQ8Tiles[p.tile].bm == 256 && kQ8Tiles[p.tile].bn == 128 && T > 256;
+  return 10000 + 100 * (loading_waves ? kQ8TileCount : p.tile) + p.splits;
+}
