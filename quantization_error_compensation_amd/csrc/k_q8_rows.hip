@@ -14,8 +14,8 @@
 // otherwise fall on the wrong side; one fp64 fma with 1.5 * 2^52 as its addend
 // multiplies, rounds half to even and leaves the integer in its low word.  Rows
 // whose maximum or scale is near fp32's small end (where p_j is no longer
-// exact, or s so coarse that codes exceed 127), or whose products leave fp32,
-// take the definition as it stands: fp64 products, a division and a clamp.
+// exact, or s so coarse that codes exceed 127), or whose products or r leave
+// fp32, take the definition as it stands: fp64 products, a division and a clamp.
 //
 // Rows of up to 2048 elements belong to one wave or, of up to 256, to a part
 // of one, and meet no barrier; wider ones to a workgroup.
@@ -312,14 +312,16 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
       }
     team.join2(top, squares);
     const double r = 1.0 / sqrt(squares / width + a.eps);
+    const float r32 = (float)r;
     bool good = squares < 1e300;  // h is finite
     const double m = (double)__uint_as_float(top);
     float s = scale_of(m * r);
-    // near fp32's small end and where a product leaves fp32 (or a weight is not
-    // finite) the products are taken again, in fp64; not for a row of zeros
+    // near fp32's small end, where a product leaves fp32 (or a weight is not finite)
+    // and where r does (mean + eps past 2^-256 or 2^252: no fp32 of 24 bits holds
+    // y's factor) the products are taken again, in fp64; not for a row of zeros
     // (padding: 4096 x 8192 of them 102 us, so 32), whose products are exact
-    const bool again =
-        good && (top >= kInfBits || (squares > 0 && (m < kSmallMax || s < kSmallScale)));
+    const bool again = good && (top >= kInfBits || !__builtin_isnormal(r32) ||
+                                (squares > 0 && (m < kSmallMax || s < kSmallScale)));
     auto product = [&](int c, int j) {
       const int i = at.lane + c * at.lanes;
       if (i >= pieces) return 0.0;
@@ -340,10 +342,6 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
     if (!live) continue;
     if (a.codes && at.lane == 0) a.scales[row] = s;
     const double ratio = r / (double)s;
-    // where mean + eps is below 2^-254 or above 2^252 no fp32 holds r with its 24
-    // bits: y is taken from the products in fp64 there too
-    const float r32 = (float)r;
-    const bool wide = again || (good && !(r >= 0x1p-126 && r <= 0x1p127));
     #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = at.lane + c * at.lanes;
@@ -362,7 +360,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
         float y[8];
         #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = p[c][j] * r32;
-        if (wide)
+        if (again)
           for (int j = 0; j < 8; ++j) y[j] = (float)(product(c, j) * r);
         u32x4 out;
         #pragma unroll
