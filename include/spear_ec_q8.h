@@ -80,11 +80,13 @@ int spear_ec_q8_dequant_f32(int32_t rows, int32_t width, const int8_t* codes, co
  *   codes, scales  as in spear_ec_q8_quantize, both or neither; at least one
  *            of y and codes is given
  * sum may be x (with x_stride == width) or residual itself; no other output
- * may overlap an input or another output.  The mean is held in 64 bits; y is off
- * by at most (1 + 2^-12) half steps of bf16, or by 2^-149 / sqrt(mean(h^2) + eps)
- * if that is more (products h * weight below fp32's normal range).  A row with
- * an infinity or NaN in h, or any row if weight holds one, gets NaN throughout y,
- * the scale NaN and codes 0; so does one whose scale leaves fp32.
+ * may overlap an input or another output.  The mean is held in 64 bits, its sum in
+ * an order that goes with rows and width: a scale or code that lies within a few
+ * 64-bit steps of a border between two may be either.  y is off by at most
+ * (1 + 2^-12) half steps of bf16, or by 2^-149 / sqrt(mean(h^2) + eps) if that is
+ * more (products h * weight below fp32's normal range).  A row with an infinity or
+ * NaN in h, or any row if weight holds one, gets NaN throughout y, the scale NaN
+ * and codes 0; so does one whose scale leaves fp32.
  */
 int spear_ec_q8_rmsnorm(int32_t rows, int32_t width, const void* x, int64_t x_stride,
                         const void* residual, void* sum, const void* weight, double eps, void* y,

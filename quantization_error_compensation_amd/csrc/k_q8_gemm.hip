@@ -12,7 +12,7 @@
 // Waves hold MT x NT results of the 32x32x32 instruction.  Operand reads take
 // LDS (MT + NT) / (MT NT) of the matrix time at 128 bytes a cycle, so the waves
 // are as square as eight of them can be; four waves of 128 x 128 would read a
-// third less, but one wave a SIMD shows every wait (2.0 against 2.45 PFLOP/s).
+// third less, but one wave a SIMD shows every wait (2.0 against 2.45 POP/s).
 // One half of the waves, one of each SIMD, issues all loads right after the
 // barrier while the other half computes, and computes when the other half is
 // done: a wave that issues loads does not issue matrix steps (gated, 3999
@@ -23,7 +23,7 @@
 // slower, and 128 x 256 gains nothing.
 //
 // What bounds it.  The largest products: the card's power.  4096 tokens of
-// 8192x8192 take 209 to 219 us (2.5 to 2.6 PFLOP/s; the library's int8 product
+// 8192x8192 take 215 to 224 us (2.45 to 2.56 POP/s; the library's int8 product
 // 2.1 here and 2.5 at best), the same on zeros 149 us, since the clock then
 // stays up.  Smaller tiles: loads into LDS, about 30 cycles a KB and unit when
 // they hit L2 and 41 from memory: a 128 x 256 tile waits 1500 to 2000 cycles for

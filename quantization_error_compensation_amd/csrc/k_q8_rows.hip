@@ -20,12 +20,13 @@
 // Rows of up to 2048 elements belong to one wave or, of up to 256, to a part
 // of one, and meet no barrier; wider ones to a workgroup.
 //
-// Norm with residual, 4096 x 8192: 40 us (5.9 TB/s), 43 to 46 with inputs and
-// outputs that the last-level cache does not hold (5.5 to 5.1 TB/s; a copy reaches
-// 4.9); without residual 22 us, where the fp64 steps of the sum and the codes show.
-// Quantization of bf16 4096 x 8192 18 us (5.6 TB/s), of fp32 11008 x 4096 38 to 41
-// us (5.9 to 5.5).  One row of 4096: 3.4 us, most of it launch, one load's latency
-// and the chain from the sums to the ratio.
+// Norm with residual, 4096 x 8192: 43 to 46 us (5.5 to 5.1 TB/s; a copy reaches
+// 4.9) over inputs and outputs that the last-level cache does not hold, 37 when the
+// same ones come again; without residual 23.5 and 20 us, where the fp64 steps of the
+// sum and the codes show.  Quantization of bf16 4096 x 8192 20 and 16 us (5.0 TB/s
+// from memory), of fp32 11008 x 4096 38 to 41 and 32.5 (5.9 to 5.5).  One row of
+// 4096: 3.4 to 3.6 us, most of it launch, one load's latency and the chain from the
+// sums to the ratio.
 #include "common.hpp"
 #include "q8_math.hpp"
 
@@ -145,8 +146,8 @@ __device__ __forceinline__ uint32_t four(const uint32_t* w) {
 }
 // The same for a p of 24 significant bits, whose ratio to s may be a tie that
 // the product with the reciprocal misses: border is set where the product, off
-// by 2^-45 at most, is that near to one.  (Dividing every element instead:
-// 11008 x 4096 from memory 62 us, so 54 to 57.)
+// by 2^-45 at most, is that near to one.  (11008 x 4096 32.5 us, 41 from memory;
+// dividing every element instead 39 and 42; 28672 x 8192 203 and 220.)
 __device__ __forceinline__ uint32_t code_or_border(float p, double inv, bool& border) {
   const double ratio = (double)p * inv, rounded = ratio + kRoundMagic;
   border |= fabs(fabs(ratio - (rounded - kRoundMagic)) - 0.5) < 0x1p-40;
@@ -375,9 +376,11 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(Q8Norm a, int 
 // 2^share lanes of a workgroup take a row, so that narrow rows fill it too
 // (100000 rows of 128: 22 us with a workgroup for each, 11.5 so).  The values, four
 // times as many bytes as the codes, are marked to leave the caches first: from
-// memory 4096 x 8192 33 -> 27 us, from the last-level cache the same.  Codes are
-// read next: so marked, quantizing 11008 x 4096 and reading it back takes 83 us
-// instead of 73.
+// memory 4096 x 8192 33 -> 27 us, from the last-level cache the same.  A read of the
+// values right behind takes back what was gained, more or less: with a conversion
+// of them to bf16 1333 x 4096 14.1 -> 13.6 us, 4096 x 4096 32.9 -> 34.8, 4096 x 8192
+// 63.5 -> 62.8, up to 512 x 4096 the same.  Codes are read next: so marked,
+// quantizing 11008 x 4096 and reading it back takes 83 us instead of 73.
 __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__ codes,
                                                       const float* __restrict__ scales,
                                                       float* __restrict__ out, int rows, int width, int share) {
@@ -407,7 +410,8 @@ struct RowPlan {
 // or 2 for fp32 (8192 x 4096 28 us, with 4 pieces 30) and in calls of fewer than
 // 2048 rows, where a row's own time counts: waves
 // that are no such number load the SIMDs unevenly, more pieces take registers
-// from a second workgroup, fewer leave lanes idle.  Norm with residual, us:
+// from a second workgroup, fewer leave lanes idle.  Norm with residual, us, the same
+// inputs again and again:
 //   8192 x 4096  2 waves of 4 pieces 37, 8 of 1 46     512 x 4096  4 waves of 2 5.5, 2 of 4 6.6
 //   4096 x 8192  4 of 4 37, 8 of 2 39, 6 of 3 48, 5 of 4 52
 //   3000 x 11008 8 of 3 38, 6 of 4 45, 4 of 6 45, 12 of 2 51
@@ -465,10 +469,10 @@ struct QuantizeLaunch {
 };
 
 // Results that the L2s (32 MB in all) would hold until the kernel's end, and only
-// then write, leave it while the kernel runs.  That pays up to about 12 MB, the next
-// read of them included; past that the next read is slower by more.  us, without
-// and with, norm to bf16 alone, norm and a quantization of its result, two norms
-// that pass a residual on:
+// then write, leave it while the kernel runs.  That pays up to about 12 MB for each
+// of sum and y, the next read of them included, and in part at 16; past that the next
+// read is slower by more.  us, without and with, norm to bf16 alone, norm and a
+// quantization of its result, two norms that pass a residual on:
 //   512 x 8192 6.1 / 5.4, 11.0 / 10.7, 16.9 / 16.1    1333 x 4096 8.1 / 7.1, 13.1 / 12.4, 20.7 / 20.1
 //   1024 x 8192 10.0 / 9.3, 16.4 / 15.9, 26.7 / 27.4  4096 x 8192 28.1 / 24.9, 45.9 / 47.9, 83.6 / 86.4
 constexpr int64_t kEarly = 6 << 20;  // elements

@@ -90,16 +90,20 @@ inline int64_t q8_tiles(const Q8Shape& s, const Q8Tile& t) {
 // fullest unit's tiles, the memory traffic that does not hide behind them (as
 // if at 10.6 TB/s), and with splits the partial sums' way through memory.  The
 // constants are fitted to 3600 timings of 12 layers at 40 to 4096 tokens; the
-// choice is 0.9% slower than the best of them on average, 15% at worst, and on
-// 7135 layers and token counts drawn at random (256 to 28672 wide) 1.8% and 44%;
-// a fit to those gains nothing on average.  Where K is no multiple of 128, rows do
-// not begin on cache lines and every load takes two: 15 to 40% longer, for all
-// shapes much alike, so that the choice is the same.  What it weighs, in us: large tiles fetch fewer bytes a product (3999 tokens gated
-// 8192->28672: 1470 with 256 x 256, 1640 with 128 x 256, 2060 with 64 x 128);
-// small ones fill the units (512 tokens 4096x4096: 14.6 with 64 x 128, 26 with
-// 256 x 128), and so do splits (512 tokens 28672->8192: 118 with 256 x 128 in 2,
-// 144 with 128 x 128 in 1; 256 tokens 8192x8192: 29 with 128 x 128 in 2, 34 with
-// 64 x 128 in 1).
+// choice is 0.9% slower than the best of them on average, 15% at worst.  On 7106
+// layers and token counts drawn at random (256 to 28672 wide) it is 1.8% slower on
+// average and by more than 20% at 1.4% of them: 553 tokens gated 13888->1664 61.8
+// us for 42.9 (44%, the worst), 136 tokens 9856->6528 35.7 for 25.4, 227 tokens
+// gated 2304->4608 18.9 for 13.6, 307 tokens 13776->3248 48.3 for 35.1, and others
+// of 80 to 620 tokens on layers of 1700 to 11000 rows; a fit to the drawn ones gains
+// nothing on average.  Where K is no multiple of 128, rows do not begin on cache
+// lines and every load takes two: 15 to 40% longer, for all shapes much alike, so
+// that the choice is the same.  What it weighs, in us: large tiles fetch fewer bytes
+// a product (3999 tokens gated 8192->28672: 1470 with 256 x 256, 1640 with 128 x
+// 256, 2060 with 64 x 128); small ones fill the units (512 tokens 4096x4096: 14.6
+// with 64 x 128, 26 with 256 x 128), and so do splits (512 tokens 28672->8192: 118
+// with 256 x 128 in 2, 144 with 128 x 128 in 1; 256 tokens 8192x8192: 29 with 128 x
+// 128 in 2, 34 with 64 x 128 in 1).
 inline Q8TilePlan plan_q8_tiles(const Q8Shape& s) {
   Q8TilePlan best{0, 1, q8_tiles(s, kQ8Tiles[0])};
   double least = 1e300;
